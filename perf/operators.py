@@ -104,7 +104,8 @@ def draw(rng):
         c["B"] = _log(rng, 2, 128)
         if kind == "fork":
             c["T"] = rng.choice([1, 1, 2, 4])
-            c["B"] = min(c["B"], 64)
+            tail = c["T"] * c["layers"] * page * Hkv * d * size * 4
+            c["B"] = max(2, min(c["B"], 64, 900_000_000 // tail))
         most = 1_000_000_000 // (c["layers"] * c["B"] * Hkv * d * size * 2)
         c["hi"] = _log(rng, 20, max(40, min(4000, most)))
         c["lo"] = rng.choice([1, max(1, c["hi"] // 2), c["hi"]])
