@@ -1,0 +1,580 @@
+// Pages of the paged key/value cache: growing, writing, forking, copying,
+// freeing and compacting.
+//
+// Each operation is a plan and, where K and V move, a data kernel. The plan
+// validates the whole list before anything changes (a refused call leaves the
+// cache as it was) and hands out free pages lowest first, so its result does
+// not depend on timing: with f_p = 1 for a free page p, the k-th new page is
+// the p with f_p = 1 and sum_{q < p} f_q = k. Plans touch little data (4
+// bytes a page, 4 bytes a table entry) and are bound by latency: one cluster of
+// eight CTAs, which can synchronise between the steps of a plan without
+// another launch and shares the scan over the pages through distributed shared
+// memory.
+//
+// The data kernels move bytes and nothing else (16-byte loads and stores, 4 KB
+// in flight a warp), bound by HBM: every byte is read once and written once.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "paged.h"
+
+namespace cg = cooperative_groups;
+
+namespace fa {
+namespace {
+
+constexpr int kPlanCtas = 8;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanAll = kPlanCtas * kPlanThreads;
+
+// Workspace of a plan, in int32 words: header, one bit per slot or page, one
+// prefix sum per list entry, two page lists and a page map.
+struct PlanWs {
+  int* bad;      // [1] the call is refused
+  int* count;    // [1] entries of the page lists
+  unsigned* bits;
+  int* at;       // [n + 1]
+  int* from;     // [pages]
+  int* to;       // [pages]
+  int* map;      // [pages]
+};
+
+constexpr int kHeaderWords = 64;
+
+__host__ __device__ inline int bit_words(int pages, int slots) {
+  return ((pages > slots ? pages : slots) + 31) / 32;
+}
+
+PlanWs plan_ws(void* ws, int pages, int slots, int n) {
+  int* w = static_cast<int*>(ws);
+  PlanWs p;
+  p.bad = w;
+  p.count = w + 1;
+  w += kHeaderWords;
+  p.bits = reinterpret_cast<unsigned*>(w);
+  w += bit_words(pages, slots);
+  p.at = w;
+  w += n + 1;
+  p.from = w;
+  p.to = w + pages;
+  p.map = w + 2 * (size_t)pages;
+  return p;
+}
+
+struct PlanShared {
+  int warp[kPlanThreads / 32];
+  int total;
+  int mine;      // this CTA's count, read by the others through the cluster
+};
+
+// Exclusive prefix sum of v over the block; `total` is the block's sum.
+__device__ int block_scan(int v, PlanShared& s, int& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s.warp[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    int y = lane < kPlanThreads / 32 ? s.warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(~0u, y, o);
+      if (lane >= o) y += z;
+    }
+    if (lane < kPlanThreads / 32) s.warp[lane] = y;
+  }
+  __syncthreads();
+  total = s.warp[kPlanThreads / 32 - 1];
+  return x - v + (w ? s.warp[w - 1] : 0);
+}
+
+// Zeroes the header and the bits; everyone sees them afterwards.
+__device__ void plan_begin(const PlanWs& p, int bits) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  if (t == 0) *p.bad = 0, *p.count = 0;
+  for (int i = t; i < bits; i += kPlanAll) p.bits[i] = 0;
+  cl.sync();
+}
+
+// Sets bit i; true if it was set already.
+__device__ __forceinline__ bool set_bit(unsigned* bits, int i) {
+  return (atomicOr(bits + (i >> 5), 1u << (i & 31)) >> (i & 31)) & 1u;
+}
+__device__ __forceinline__ bool get_bit(const unsigned* bits, int i) {
+  return (__ldcg(bits + (i >> 5)) >> (i & 31)) & 1u;
+}
+
+__device__ __forceinline__ bool in_range(int i, int n) { return (unsigned)i < (unsigned)n; }
+
+// Calls emit(rank, i) for every i in [0, n) with pred(i), rank counting from 0 in
+// the order of i, for ranks below `limit`; returns how many i there are. The
+// whole cluster takes part; each CTA has a contiguous part of the range.
+template <class Pred, class Emit>
+__device__ int cluster_pick(int n, int limit, PlanShared& s, Pred pred, Emit emit) {
+  cg::cluster_group cl = cg::this_cluster();
+  constexpr int kPer = 4;
+  const int per = ((n + kPlanCtas - 1) / kPlanCtas + kPer - 1) / kPer * kPer;
+  const int lo = min(n, (int)blockIdx.x * per), hi = min(n, lo + per);
+  int mine = 0;
+  for (int i = lo + threadIdx.x; i < hi; i += kPlanThreads) mine += pred(i) ? 1 : 0;
+  int total;
+  block_scan(mine, s, total);
+  if (threadIdx.x == 0) s.mine = total;
+  cl.sync();
+  int before = 0, all = 0;
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int v = *cl.map_shared_rank(&s.mine, r);
+    if (r < (int)blockIdx.x) before += v;
+    all += v;
+  }
+  cl.sync();
+  for (int base = lo; base < hi && before < limit; base += kPlanThreads * kPer) {
+    const int i0 = base + threadIdx.x * kPer;
+    bool f[kPer];
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      f[j] = i0 + j < hi && pred(i0 + j);
+      c += f[j] ? 1 : 0;
+    }
+    int rank = before + block_scan(c, s, total);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (f[j]) {
+        if (rank < limit) emit(rank, i0 + j);
+        ++rank;
+      }
+    before += total;
+  }
+  return all;
+}
+
+// at[i] = sum of need(i') for i' < i, at[n] = the sum of all, saturated at 2^30.
+// The first CTA does it; the others meet it at the next cluster barrier.
+template <class Need>
+__device__ void list_scan(int n, int* at, PlanShared& s, Need need) {
+  if (blockIdx.x == 0) {
+    int base = 0;
+    for (int b = 0; b < n; b += kPlanThreads) {
+      const int i = b + threadIdx.x;
+      int total;
+      const int x = block_scan(i < n ? need(i) : 0, s, total);
+      if (i < n) at[i] = min(base + x, 1 << 30);
+      base = min(base + total, 1 << 30);
+    }
+    if (threadIdx.x == 0) at[n] = base;
+  }
+}
+
+__device__ __forceinline__ void refuse(const CacheView& c) { atomicOr(c.err, (unsigned)kErrCache); }
+
+// ---------------------------------------------------------------- extend
+
+__device__ __forceinline__ int new_tokens(const int* cu, int tokens, int i) {
+  return cu ? cu[i + 1] - cu[i] : tokens;
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    extend_kernel(CacheView c, const int* seqs, int n, const int* cu, int tokens, int* pos,
+                  PlanWs p) {
+  __shared__ PlanShared s;
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  const int ps = 1 << c.page_log2;
+  const long long most = (long long)c.width * ps;
+  plan_begin(p, bit_words(0, c.slots));
+  // sequence i: its slot, length and new tokens; false if any is wrong
+  auto get = [&](int i, int& slot, int& len, int& more) {
+    slot = seqs[i];
+    more = new_tokens(cu, tokens, i);
+    if (!in_range(slot, c.slots) || more < 0) return false;
+    len = c.lens[slot];
+    return len >= 0 && (long long)len + more <= most;
+  };
+  auto need = [&](int i) {
+    int slot, len, more;
+    if (!get(i, slot, len, more)) return 0;
+    return ((len + more + ps - 1) >> c.page_log2) - ((len + ps - 1) >> c.page_log2);
+  };
+  for (int i = t; i < n; i += kPlanAll) {
+    int slot, len, more;
+    if (!get(i, slot, len, more) || set_bit(p.bits, slot)) *p.bad = 1;
+  }
+  list_scan(n, p.at, s, need);
+  cl.sync();
+  const int total = __ldcg(p.at + n);
+  int found = 0;
+  if (total > 0 && total <= c.pages)
+    found = cluster_pick(c.pages, total, s, [&](int i) { return __ldcg(c.refs + i) == 0; },
+                         [&](int k, int i) { p.to[k] = i; });
+  const bool bad = __ldcg(p.bad) || found < total;
+  cl.sync();   // the lists are complete, and everyone has read what follows changes
+  if (bad) {
+    for (int i = t; i < n; i += kPlanAll) pos[i] = -1;
+    if (t == 0) refuse(c);
+    return;
+  }
+  for (int k = t; k < total; k += kPlanAll) {
+    int a = 0, b = n - 1;   // the sequence that the k-th new page belongs to
+    while (a < b) {
+      const int m = (a + b + 1) >> 1;
+      if (__ldcg(p.at + m) <= k) a = m; else b = m - 1;
+    }
+    const int slot = seqs[a], page = __ldcg(p.to + k);
+    const int have = (__ldcg(c.lens + slot) + ps - 1) >> c.page_log2;
+    c.table[(size_t)slot * c.width + have + k - __ldcg(p.at + a)] = page;
+    c.refs[page] = 1;
+  }
+  cl.sync();
+  for (int i = t; i < n; i += kPlanAll) {
+    const int slot = seqs[i], len = __ldcg(c.lens + slot);
+    pos[i] = len;
+    c.lens[slot] = len + new_tokens(cu, tokens, i);
+  }
+}
+
+// ---------------------------------------------------------------- write
+
+// One warp per token: its position follows from the list, then 16-byte pieces of
+// its Hkv heads go to the heads' rows of the page.
+__global__ void __launch_bounds__(256)
+    write_kernel(CacheView c, char* lk, char* lv, const char* K, const char* V, const int* seqs,
+                 const int* pos, int n, const int* cu, int total) {
+  const int lane = threadIdx.x & 31;
+  const int row_vecs = c.row_bytes >> 4;              // 16-byte pieces of a head's row
+  const int vecs = c.Hkv * row_vecs;
+  const int ps_mask = (1 << c.page_log2) - 1;
+  const int warps = gridDim.x * (blockDim.x >> 5);
+  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < total; r += warps) {
+    int i, j;
+    if (cu) {
+      int a = 0, b = n - 1;                           // the last sequence that begins at or before r
+      while (a < b) {
+        const int m = (a + b + 1) >> 1;
+        if (cu[m] <= r) a = m; else b = m - 1;
+      }
+      i = a;
+      j = r - cu[a];
+      if (j < 0 || r >= cu[a + 1]) continue;          // no sequence's row
+    } else {
+      const int each = total / n;
+      i = r / each;
+      j = r - i * each;
+    }
+    const int p0 = pos[i];
+    if (p0 < 0) continue;
+    const int slot = seqs[i];
+    bool ok = in_range(slot, c.slots) && j <= 0x7fffffff - p0;
+    const int at = p0 + j;
+    int page = -1;
+    if (ok) ok = at < c.lens[slot] && (at >> c.page_log2) < c.width;
+    if (ok) {
+      page = c.table[(size_t)slot * c.width + (at >> c.page_log2)];
+      ok = in_range(page, c.pages) && c.refs[page] == 1;
+    }
+    if (!ok) {
+      if (lane == 0) refuse(c);
+      continue;
+    }
+    const size_t dst0 = (size_t)page * c.page_stride + (size_t)(at & ps_mask) * c.row_bytes;
+    const size_t src0 = (size_t)r * c.Hkv * c.row_bytes;
+    for (int v = lane; v < vecs; v += 32) {
+      const int h = v / row_vecs;
+      const size_t dst = dst0 + (size_t)h * c.head_bytes + (size_t)(v - h * row_vecs) * 16;
+      const int4 x = __ldcs(reinterpret_cast<const int4*>(K + src0) + v);
+      const int4 y = __ldcs(reinterpret_cast<const int4*>(V + src0) + v);
+      *reinterpret_cast<int4*>(lk + dst) = x;
+      *reinterpret_cast<int4*>(lv + dst) = y;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- page data
+
+// Copies pages from[k] -> to[k] for k < *count in all layers of K and V: a warp
+// takes 4 KB pieces, eight 16-byte loads a lane in flight.
+__device__ void copy_pages(const CacheView& c, const int* from, const int* to, int count) {
+  constexpr int kPiece = 4096;
+  const int lane = threadIdx.x & 31;
+  const int pieces = (c.page_bytes + kPiece - 1) / kPiece;
+  const long long units = (long long)count * c.layers * 2 * pieces;
+  const int per_block = blockDim.x >> 5;
+  const long long warps = (long long)gridDim.x * per_block;
+  for (long long u = (long long)blockIdx.x * per_block + (threadIdx.x >> 5); u < units;
+       u += warps) {
+    const long long q = u / pieces;
+    const int piece = (int)(u - q * pieces);
+    const long long pair = q >> 1;                    // (layer, k), k fastest
+    const int layer = (int)(pair / count);
+    const int k = (int)(pair - (long long)layer * count);
+    const int a = from[k], b = to[k];
+    if (!in_range(a, c.pages) || !in_range(b, c.pages) || a == b) continue;
+    char* base = ((q & 1) ? c.V : c.K) + layer * c.layer_stride + (size_t)piece * kPiece;
+    const int4* src = reinterpret_cast<const int4*>(base + a * c.page_stride);
+    int4* dst = reinterpret_cast<int4*>(base + b * c.page_stride);
+    const int left = (min(kPiece, c.page_bytes - piece * kPiece)) >> 4;
+    int4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < left) x[i] = __ldcs(src + lane + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < left) __stcs(dst + lane + 32 * i, x[i]);
+  }
+}
+
+__global__ void __launch_bounds__(256) copy_kernel(CacheView c, PlanWs p, const int* from,
+                                                   const int* to, int n) {
+  if (*p.bad) return;
+  copy_pages(c, from, to, n);
+}
+
+// ---------------------------------------------------------------- fork
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    fork_plan_kernel(CacheView c, const int* src, const int* dst, int n, PlanWs p) {
+  __shared__ PlanShared s;
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  const int ps = 1 << c.page_log2;
+  const long long most = (long long)c.width * ps;
+  plan_begin(p, bit_words(0, c.slots));
+  for (int i = t; i < n; i += kPlanAll) {
+    const int d = dst[i];
+    if (!in_range(d, c.slots) || set_bit(p.bits, d) || c.lens[d] != 0) *p.bad = 1;
+  }
+  cl.sync();
+  // a partly filled last page needs a copy of its own
+  auto need = [&](int i) {
+    const int a = src[i];
+    return in_range(a, c.slots) && (c.lens[a] & (ps - 1)) ? 1 : 0;
+  };
+  for (int i = t; i < n; i += kPlanAll) {
+    const int a = src[i];
+    if (!in_range(a, c.slots) || get_bit(p.bits, a) || c.lens[a] < 0 || c.lens[a] > most)
+      *p.bad = 1;
+  }
+  list_scan(n, p.at, s, need);
+  cl.sync();
+  const int total = __ldcg(p.at + n);
+  int found = 0;
+  if (total > 0 && total <= c.pages)
+    found = cluster_pick(c.pages, total, s, [&](int i) { return c.refs[i] == 0; },
+                         [&](int k, int i) { p.to[k] = i; });
+  if (!__ldcg(p.bad) && found >= total) {
+    for (int i = t; i < n; i += kPlanAll)
+      if (need(i)) {
+        const int a = src[i];
+        p.from[p.at[i]] = c.table[(size_t)a * c.width + (c.lens[a] >> c.page_log2)];
+      }
+    if (t == 0) *p.count = total;
+  } else {
+    cl.sync();   // every CTA has read `bad` before it is set for want of pages
+    if (t == 0) {
+      *p.bad = 1;
+      refuse(c);
+    }
+    return;
+  }
+  cl.sync();
+}
+
+__global__ void __launch_bounds__(256)
+    fork_kernel(CacheView c, const int* src, const int* dst, int n, PlanWs p) {
+  if (*p.bad) return;
+  const int ps = 1 << c.page_log2;
+  const long long all = (long long)gridDim.x * blockDim.x;
+  const long long entries = (long long)n * c.width;
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < entries; e += all) {
+    const int i = (int)(e / c.width), w = (int)(e - (long long)i * c.width);
+    const int a = src[i], d = dst[i], len = c.lens[a];
+    const int full = len >> c.page_log2;
+    int page = -1;
+    if (w < full) {
+      page = c.table[(size_t)a * c.width + w];
+      if (in_range(page, c.pages)) atomicAdd(c.refs + page, 1);
+    } else if (w == full && (len & (ps - 1))) {
+      page = p.to[p.at[i]];
+      c.refs[page] = 1;
+    }
+    c.table[(size_t)d * c.width + w] = page;
+    if (w == 0) c.lens[d] = len;
+  }
+  copy_pages(c, p.from, p.to, *p.count);
+}
+
+// ---------------------------------------------------------------- free
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    free_kernel(CacheView c, const int* seqs, int n, PlanWs p) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  plan_begin(p, bit_words(0, c.slots));
+  for (int i = t; i < n; i += kPlanAll) {
+    const int slot = seqs[i];
+    if (!in_range(slot, c.slots) || set_bit(p.bits, slot)) *p.bad = 1;
+  }
+  cl.sync();
+  if (__ldcg(p.bad)) {
+    if (t == 0) refuse(c);
+    return;
+  }
+  const long long entries = (long long)n * c.width;
+  for (long long e = t; e < entries; e += kPlanAll) {
+    const int i = (int)(e / c.width), w = (int)(e - (long long)i * c.width);
+    const int slot = seqs[i];
+    int* at = c.table + (size_t)slot * c.width + w;
+    const int page = *at;
+    if (in_range(page, c.pages)) atomicSub(c.refs + page, 1);
+    if (page != -1) *at = -1;
+    if (w == 0) c.lens[slot] = 0;
+  }
+}
+
+// ---------------------------------------------------------------- copy
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    copy_plan_kernel(CacheView c, const int* src, const int* dst, int n, PlanWs p) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  plan_begin(p, bit_words(c.pages, 0));
+  for (int i = t; i < n; i += kPlanAll) {
+    const int d = dst[i];
+    if (!in_range(d, c.pages) || set_bit(p.bits, d)) *p.bad = 1;
+  }
+  cl.sync();
+  for (int i = t; i < n; i += kPlanAll) {
+    const int a = src[i];
+    if (!in_range(a, c.pages) || get_bit(p.bits, a)) *p.bad = 1;
+  }
+  cl.sync();
+  if (t == 0 && __ldcg(p.bad)) refuse(c);
+}
+
+// ---------------------------------------------------------------- compact
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    compact_plan_kernel(CacheView c, PlanWs p) {
+  __shared__ PlanShared s;
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  plan_begin(p, 0);
+  const int live = cluster_pick(c.pages, 0, s, [&](int i) { return c.refs[i] > 0; },
+                                [](int, int) {});
+  // as many pages in use lie behind the first `live` as there are holes among them
+  const int moves = cluster_pick(c.pages, c.pages, s,
+                                 [&](int i) { return i >= live && c.refs[i] > 0; },
+                                 [&](int k, int i) { p.from[k] = i; });
+  cluster_pick(c.pages, c.pages, s, [&](int i) { return i < live && c.refs[i] <= 0; },
+               [&](int k, int i) { p.to[k] = i; });
+  for (int i = t; i < c.pages; i += kPlanAll) p.map[i] = i;
+  cl.sync();
+  for (int k = t; k < moves; k += kPlanAll) {
+    const int a = __ldcg(p.from + k), b = __ldcg(p.to + k);
+    p.map[a] = b;
+    c.refs[b] = c.refs[a];
+    c.refs[a] = 0;
+  }
+  if (t == 0) *p.count = moves;
+}
+
+__global__ void __launch_bounds__(256) compact_kernel(CacheView c, PlanWs p) {
+  const int count = *p.count;
+  if (count == 0) return;
+  const long long all = (long long)gridDim.x * blockDim.x;
+  const long long entries = (long long)c.slots * c.width;
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < entries; e += all) {
+    const int page = c.table[e];
+    if (in_range(page, c.pages)) {
+      const int to = p.map[page];
+      if (to != page) c.table[e] = to;
+    }
+  }
+  copy_pages(c, p.from, p.to, count);
+}
+
+// Enough blocks of 256 threads to fill the device, fewer for little work.
+int data_blocks(long long threads) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  long long b = (threads + 255) / 256;
+  const long long most = (long long)sms * 8;
+  return (int)(b < 1 ? 1 : (b > most ? most : b));
+}
+
+// Threads that copying n pages in all layers keeps busy (128 bytes a thread).
+long long copy_threads(const CacheView& c, long long n) {
+  return n * c.layers * 2 * ((c.page_bytes + 127) / 128);
+}
+
+cudaError_t done() {
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_workspace_bytes(int pages, int slots, int n) {
+  return 4 * ((size_t)kHeaderWords + bit_words(pages, slots) + (size_t)n + 1 +
+              3 * (size_t)pages);
+}
+
+cudaError_t cache_extend(const CacheView& c, const int* seqs, int n, const int* cu, int tokens,
+                         int* pos, void* ws, cudaStream_t st) {
+  extend_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, seqs, n, cu, tokens, pos,
+                                                    plan_ws(ws, c.pages, c.slots, n));
+  return done();
+}
+
+cudaError_t cache_write(const CacheView& c, int layer, const void* K, const void* V,
+                        const int* seqs, const int* pos, int n, const int* cu, int total,
+                        cudaStream_t st) {
+  char* lk = c.K + layer * c.layer_stride;
+  char* lv = c.V + layer * c.layer_stride;
+  write_kernel<<<data_blocks((long long)total * 32), 256, 0, st>>>(
+      c, lk, lv, static_cast<const char*>(K), static_cast<const char*>(V), seqs, pos, n, cu,
+      total);
+  return done();
+}
+
+cudaError_t cache_fork(const CacheView& c, const int* src, const int* dst, int n, void* ws,
+                       cudaStream_t st) {
+  const PlanWs p = plan_ws(ws, c.pages, c.slots, n);
+  fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, src, dst, n, p);
+  if (cudaError_t e = done()) return e;
+  const long long entries = (long long)n * c.width, copies = copy_threads(c, n);
+  fork_kernel<<<data_blocks(entries > copies ? entries : copies), 256, 0, st>>>(c, src, dst, n, p);
+  return done();
+}
+
+cudaError_t cache_free(const CacheView& c, const int* seqs, int n, void* ws, cudaStream_t st) {
+  free_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, seqs, n, plan_ws(ws, c.pages, c.slots, n));
+  return done();
+}
+
+cudaError_t cache_copy(const CacheView& c, const int* src, const int* dst, int n, void* ws,
+                       cudaStream_t st) {
+  const PlanWs p = plan_ws(ws, c.pages, c.slots, n);
+  copy_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, src, dst, n, p);
+  if (cudaError_t e = done()) return e;
+  copy_kernel<<<data_blocks(copy_threads(c, n)), 256, 0, st>>>(c, p, src, dst, n);
+  return done();
+}
+
+cudaError_t cache_compact(const CacheView& c, void* ws, cudaStream_t st) {
+  const PlanWs p = plan_ws(ws, c.pages, c.slots, 0);
+  compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, p);
+  if (cudaError_t e = done()) return e;
+  const long long entries = (long long)c.slots * c.width, copies = copy_threads(c, c.pages);
+  compact_kernel<<<data_blocks(entries > copies ? entries : copies), 256, 0, st>>>(c, p);
+  return done();
+}
+
+}  // namespace fa

@@ -16,6 +16,7 @@ namespace fa {
 
 static thread_local int t_launches = 0;
 void count_launch(int n) { t_launches += n; }
+void reset_launch_count() { t_launches = 0; }
 
 // Wait-limit test hook (fa_debug_set_stall): kernel families with an injected
 // wait and its limit in SM cycles. Process-wide; read at each launch.
@@ -125,11 +126,12 @@ const char* fa_status_string(int s) {
     case FA_ERR_UNSUPPORTED: return "FA_ERR_UNSUPPORTED";
     case FA_ERR_CUDA: return "FA_ERR_CUDA";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
+    case FA_ERR_CACHE: return "FA_ERR_CACHE";
     default: return "FA_ERR_UNKNOWN";
   }
 }
 
-int fa_version(void) { return 10000; }
+int fa_version(void) { return 10100; }
 
 int fa_last_launch_count(void) { return t_launches; }
 
@@ -482,7 +484,8 @@ fa_status fa_get_device_error(void* workspace, void* stream) {
   if (word == 0) return FA_OK;
   if (cudaMemsetAsync(workspace, 0, sizeof(word), st) != cudaSuccess) return FA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
-  return (word & kErrTimeout) ? FA_ERR_TIMEOUT : FA_ERR_CUDA;
+  if (word & kErrTimeout) return FA_ERR_TIMEOUT;
+  return (word & kErrCache) ? FA_ERR_CACHE : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -56,7 +56,7 @@ struct Problem {
 };
 
 // Error-word bits set by kernels.
-enum : unsigned { kErrTimeout = 1u, kErrBounds = 2u };
+enum : unsigned { kErrTimeout = 1u, kErrBounds = 2u, kErrCache = 4u };
 
 // Kernel families of the wait-limit test hook (fa_debug_set_stall).
 enum : int { kStallFwd = 1, kStallBwd = 2, kStallDq = 4 };
@@ -66,6 +66,7 @@ long long debug_stall_cycles(int family);
 
 // Counts launches made by the current ABI call (thread-local).
 void count_launch(int n = 1);
+void reset_launch_count();
 
 // CUDA-core kernels (fp32 arithmetic). simt_kernels.cu
 cudaError_t simt_fwd(const Problem& p);

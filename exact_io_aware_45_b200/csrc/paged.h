@@ -1,0 +1,77 @@
+// Internal interface of the paged key/value cache: the device's view of a
+// cache, and the work division of the attention kernels that read it.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa.h"
+#include "internal.h"
+
+namespace fa {
+
+// A cache as the kernels see it; strides in bytes.
+struct CacheView {
+  char* K;
+  char* V;
+  long long layer_stride, page_stride;
+  int layers, pages, width, slots;
+  int page_log2;       // page_size = 1 << page_log2
+  int head_bytes;      // page_size * d * element size: one head's rows of one page
+  int page_bytes;      // Hkv * head_bytes
+  int row_bytes;       // d * element size
+  int Hkv, d;
+  int* table;
+  int* lens;
+  int* refs;
+  unsigned* err;
+};
+
+cudaError_t cache_extend(const CacheView& c, const int* seqs, int n, const int* cu, int tokens,
+                         int* pos, void* ws, cudaStream_t st);
+cudaError_t cache_write(const CacheView& c, int layer, const void* K, const void* V,
+                        const int* seqs, const int* pos, int n, const int* cu, int total,
+                        cudaStream_t st);
+cudaError_t cache_fork(const CacheView& c, const int* src, const int* dst, int n, void* ws,
+                       cudaStream_t st);
+cudaError_t cache_free(const CacheView& c, const int* seqs, int n, void* ws, cudaStream_t st);
+cudaError_t cache_copy(const CacheView& c, const int* src, const int* dst, int n, void* ws,
+                       cudaStream_t st);
+cudaError_t cache_compact(const CacheView& c, void* ws, cudaStream_t st);
+size_t cache_workspace_bytes(int pages, int slots, int n);
+
+// One phase of an attention call: `items` row tiles (of up to `rows` packed
+// query rows that share a KV head), each over its own key tiles of `tile` keys,
+// laid end to end and cut into `n` even ranges, one per CTA.
+struct Phase {
+  int rows = 0;        // query rows per item, at most
+  int tile = 0;        // keys per tile
+  int rt = 0;          // row tiles per (sequence, KV head); per KV head in the shared phase
+  int n = 0;           // CTAs
+  int items = 0;
+  float* o = nullptr;  // partial results: [items + n][rows][d], normalised
+  float* lse = nullptr;  // [items + n][rows], base 2
+};
+
+struct PagedArgs {
+  CacheView c;
+  const char* K;       // the layer's pages
+  const char* V;
+  const void* Q;
+  void* O;
+  float* LSE;
+  const int* seqs;
+  int B, T, Hq, G;
+  int TG;              // T * G: packed query rows of one sequence and KV head
+  int shared;          // tokens of the shared prefix
+  int causal, wl;
+  float scale, softcap;
+  Phase own, pre;
+};
+
+// Kernel families. Each runs one phase (`pre`: the shared prefix).
+cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
+// Joins the partial results of both phases.
+cudaError_t paged_join(const PagedArgs& a, int dtype, cudaStream_t st);
+
+}  // namespace fa

@@ -1,0 +1,287 @@
+// C ABI of the paged cache and its attention: argument checks, workspace
+// layout, kernel choice. See include/fa.h for the contract.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "paged.h"
+
+namespace fa {
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+bool aligned(const void* p, unsigned to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0;
+}
+
+int elem_bytes(int dtype) { return dtype == FA_F32 ? 4 : 2; }
+
+// Checks a cache's description and fills the kernels' view of it.
+fa_status view_of(const fa_cache* c, CacheView& v) {
+  if (!c) return FA_ERR_INVALID_ARG;
+  if (c->layers <= 0 || c->pages <= 0 || c->Hkv <= 0 || c->seqs <= 0 || c->seq_pages <= 0)
+    return FA_ERR_INVALID_ARG;
+  if (c->dtype != FA_F32 && c->dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+  if (c->d <= 0 || c->page_size <= 0) return FA_ERR_INVALID_ARG;
+  if (c->d != 16 && c->d != 32 && c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  int lg = 4;
+  while (lg < 8 && (1 << lg) != c->page_size) ++lg;
+  if (lg == 8) return FA_ERR_UNSUPPORTED;
+  const long long es = elem_bytes(c->dtype);
+  const long long page = (long long)c->Hkv * c->page_size * c->d;
+  if (page * es >= (1ll << 30) || c->pages >= (1 << 28) || c->layers >= (1 << 16) ||
+      (long long)c->seq_pages * c->page_size >= (1ll << 30) ||
+      (long long)c->seqs * c->seq_pages >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  if (c->page_stride < page || (c->layers > 1 && c->layer_stride < page))
+    return FA_ERR_INVALID_ARG;
+  if (c->page_stride >= (1ll << 36) || c->layer_stride >= (1ll << 44)) return FA_ERR_UNSUPPORTED;
+  if ((c->page_stride * es) & 15 || (c->layers > 1 && ((c->layer_stride * es) & 15)))
+    return FA_ERR_INVALID_ARG;
+  if (!c->K || !c->V || !c->table || !c->lens || !c->refs || !c->err) return FA_ERR_INVALID_ARG;
+  if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->table, 4) || !aligned(c->lens, 4) ||
+      !aligned(c->refs, 4) || !aligned(c->err, 4))
+    return FA_ERR_INVALID_ARG;
+  v.K = static_cast<char*>(c->K);
+  v.V = static_cast<char*>(c->V);
+  v.layer_stride = c->layer_stride * es;
+  v.page_stride = c->page_stride * es;
+  v.layers = c->layers;
+  v.pages = c->pages;
+  v.width = c->seq_pages;
+  v.slots = c->seqs;
+  v.page_log2 = lg;
+  v.row_bytes = (int)(c->d * es);
+  v.head_bytes = c->page_size * v.row_bytes;
+  v.page_bytes = c->Hkv * v.head_bytes;
+  v.Hkv = c->Hkv;
+  v.d = c->d;
+  v.table = c->table;
+  v.lens = c->lens;
+  v.refs = c->refs;
+  v.err = c->err;
+  return FA_OK;
+}
+
+fa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// Checks of a list of n int32 entries, and of the workspace.
+bool bad_list(const int* p, int n) { return n > 0 && (!p || !aligned(p, 4)); }
+fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
+  if (!ws || !aligned(ws, 16) || bytes < cache_workspace_bytes(v.pages, v.slots, n))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 148;
+  return n;
+}
+
+// Blocks of the CUDA-core kernel per SM, its rows and keys per tile.
+constexpr int kSimtPerSm = 4, kSimtRows = 8, kSimtTile = 32;
+
+// The work division of a call. It depends on sizes only, so the workspace query
+// and the call agree.
+void plan(PagedArgs& a, int sms) {
+  const int R = a.B * a.TG;
+  a.own.rows = kSimtRows;
+  a.own.tile = kSimtTile;
+  a.own.rt = (a.TG + kSimtRows - 1) / kSimtRows;
+  a.own.items = a.B * a.c.Hkv * a.own.rt;
+  a.own.n = sms * kSimtPerSm;
+  a.pre = Phase();
+  a.pre.rows = kSimtRows;
+  a.pre.tile = kSimtTile;
+  if (a.shared) {
+    a.pre.rt = (R + kSimtRows - 1) / kSimtRows;
+    a.pre.items = a.c.Hkv * a.pre.rt;
+    a.pre.n = sms * kSimtPerSm;
+  }
+}
+
+size_t phase_bytes(const Phase& p, int d, size_t* lse_at) {
+  const size_t rows = (size_t)(p.items + p.n) * p.rows;
+  *lse_at = align256(rows * d * 4);
+  return *lse_at + align256(rows * 4);
+}
+
+fa_status check_fwd(const CacheView& v, int B, int T, int Hq, int shared) {
+  if (B < 0 || T < 0 || Hq <= 0 || Hq % v.Hkv != 0 || shared < 0) return FA_ERR_INVALID_ARG;
+  if (shared & ((1 << v.page_log2) - 1)) return FA_ERR_INVALID_ARG;
+  if (shared > v.width << v.page_log2) return FA_ERR_INVALID_ARG;
+  // packed rows, items and table indexes stay in int
+  if ((long long)B * T * Hq >= (1ll << 28) || (long long)T * (Hq / v.Hkv) >= (1ll << 20))
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+void sizes(PagedArgs& a, const CacheView& v, int B, int T, int Hq, int shared) {
+  a.c = v;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.G = Hq / v.Hkv;
+  a.TG = T * a.G;
+  a.shared = shared;
+}
+
+fa_status fwd(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
+              const int* seqs, int B, int T, int Hq, int shared, float scale, int causal,
+              int window_left, float softcap, void* ws, size_t ws_bytes, void* stream) {
+  reset_launch_count();
+  PagedArgs a;
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (fa_status s = check_fwd(v, B, T, Hq, shared)) return s;
+  if (layer < 0 || layer >= v.layers || (causal != 0 && causal != 1) || window_left < -1 ||
+      !isfinite(scale) || !isfinite(softcap) || softcap < 0.f)
+    return FA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return FA_OK;
+  if (!seqs && B > v.slots) return FA_ERR_INVALID_ARG;
+  if (!Q || !O || !LSE || !aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) ||
+      !aligned(seqs, 4))
+    return FA_ERR_INVALID_ARG;
+  sizes(a, v, B, T, Hq, shared);
+  a.K = v.K + layer * v.layer_stride;
+  a.V = v.V + layer * v.layer_stride;
+  a.Q = Q;
+  a.O = O;
+  a.LSE = LSE;
+  a.seqs = seqs;
+  a.causal = causal;
+  a.wl = window_left;
+  a.scale = scale;
+  a.softcap = softcap;
+  plan(a, sm_count());
+  size_t own_lse, pre_lse;
+  const size_t own = phase_bytes(a.own, v.d, &own_lse), pre = phase_bytes(a.pre, v.d, &pre_lse);
+  if (!ws || !aligned(ws, 16) || ws_bytes < own + pre) return FA_ERR_INVALID_ARG;
+  char* w = static_cast<char*>(ws);
+  a.own.o = reinterpret_cast<float*>(w);
+  a.own.lse = reinterpret_cast<float*>(w + own_lse);
+  a.pre.o = reinterpret_cast<float*>(w + own);
+  a.pre.lse = reinterpret_cast<float*>(w + own + pre_lse);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (shared)
+    if (cudaError_t e = paged_simt(a, true, cache->dtype, st)) return from_cuda(e);
+  if (cudaError_t e = paged_simt(a, false, cache->dtype, st)) return from_cuda(e);
+  return from_cuda(paged_join(a, cache->dtype, st));
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_cache_workspace_size(const fa_cache* cache, int n) {
+  CacheView v;
+  if (n < 0 || view_of(cache, v) != FA_OK) return 0;
+  return cache_workspace_bytes(v.pages, v.slots, n);
+}
+
+fa_status fa_cache_extend(const fa_cache* cache, const int* seqs, int n, const int* cu_seqlens,
+                          int tokens, int* pos, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  reset_launch_count();
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (n < 0 || n > v.slots || bad_list(seqs, n) || bad_list(pos, n) || !aligned(cu_seqlens, 4) ||
+      (!cu_seqlens && tokens < 0))
+    return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (fa_status s = check_ws(v, n, workspace, workspace_bytes)) return s;
+  return from_cuda(cache_extend(v, seqs, n, cu_seqlens, tokens, pos, workspace,
+                                static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_write(const fa_cache* cache, int layer, const void* K, const void* V,
+                         const int* seqs, const int* pos, int n, const int* cu_seqlens,
+                         int total, void* stream) {
+  reset_launch_count();
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (layer < 0 || layer >= v.layers || n < 0 || total < 0 || bad_list(seqs, n) ||
+      bad_list(pos, n) || !aligned(cu_seqlens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (n == 0 || total == 0) return FA_OK;
+  if (!cu_seqlens && total % n != 0) return FA_ERR_INVALID_ARG;
+  if (!K || !V || !aligned(K, 16) || !aligned(V, 16)) return FA_ERR_INVALID_ARG;
+  return from_cuda(cache_write(v, layer, K, V, seqs, pos, n, cu_seqlens, total,
+                               static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_fork(const fa_cache* cache, const int* src, const int* dst, int n,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  reset_launch_count();
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (n < 0 || n > v.slots || bad_list(src, n) || bad_list(dst, n)) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (fa_status s = check_ws(v, n, workspace, workspace_bytes)) return s;
+  return from_cuda(cache_fork(v, src, dst, n, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_free(const fa_cache* cache, const int* seqs, int n, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  reset_launch_count();
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (n < 0 || n > v.slots || bad_list(seqs, n)) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (fa_status s = check_ws(v, n, workspace, workspace_bytes)) return s;
+  return from_cuda(cache_free(v, seqs, n, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_copy(const fa_cache* cache, const int* src, const int* dst, int n,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  reset_launch_count();
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (n < 0 || n > v.pages || bad_list(src, n) || bad_list(dst, n)) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (fa_status s = check_ws(v, n, workspace, workspace_bytes)) return s;
+  return from_cuda(cache_copy(v, src, dst, n, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_compact(const fa_cache* cache, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  reset_launch_count();
+  CacheView v;
+  if (fa_status s = view_of(cache, v)) return s;
+  if (fa_status s = check_ws(v, 0, workspace, workspace_bytes)) return s;
+  return from_cuda(cache_compact(v, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_paged_workspace_size(const fa_cache* cache, int B, int T, int Hq, int shared) {
+  CacheView v;
+  if (view_of(cache, v) != FA_OK || check_fwd(v, B, T, Hq, shared) != FA_OK) return 0;
+  PagedArgs a;
+  sizes(a, v, B, T, Hq, shared);
+  plan(a, sm_count());
+  size_t at;
+  return phase_bytes(a.own, v.d, &at) + phase_bytes(a.pre, v.d, &at);
+}
+
+fa_status fa_fwd_paged(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
+                       const int* seqs, int B, int T, int Hq, float scale, int causal,
+                       int window_left, float softcap, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  return fwd(cache, layer, Q, O, LSE, seqs, B, T, Hq, 0, scale, causal, window_left, softcap,
+             workspace, workspace_bytes, stream);
+}
+
+fa_status fa_fwd_shared(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
+                        const int* seqs, int B, int T, int Hq, int shared, float scale,
+                        int causal, int window_left, float softcap, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  return fwd(cache, layer, Q, O, LSE, seqs, B, T, Hq, shared, scale, causal, window_left,
+             softcap, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

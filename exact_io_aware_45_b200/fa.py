@@ -19,7 +19,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 # different tile parameters); the default is the in-tree build.
 LIB_PATH = os.environ.get("FA_LIBRARY") or os.path.join(PKG, "_lib", "libfa.so")
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_CACHE = range(6)
 FA_F32, FA_BF16 = 0, 1
 PATH_AUTO, PATH_SIMT, PATH_TC = 0, 1, 2
 FA_STALL_FWD, FA_STALL_BWD, FA_STALL_DQ = 1, 2, 4
@@ -30,7 +30,10 @@ EXPORTS = ("fa_status_string", "fa_version", "fa_fwd_workspace_size", "fa_bwd_wo
            "fa_bwd_finalize", "fa_last_launch_count", "fa_get_device_error", "fa_exp2_fma",
            "fa_fwd_varlen", "fa_bwd_varlen", "fa_bwd_varlen_workspace_size",
            "fa_bwd_deterministic", "fa_fwd_window", "fa_bwd_window", "fa_bwd_noalloc",
-           "fa_debug_set_stall", "fa_fwd_mod", "fa_bwd_mod")
+           "fa_debug_set_stall", "fa_fwd_mod", "fa_bwd_mod", "fa_cache_workspace_size",
+           "fa_cache_extend", "fa_cache_write", "fa_cache_fork", "fa_cache_free",
+           "fa_cache_copy", "fa_cache_compact", "fa_fwd_paged", "fa_fwd_shared",
+           "fa_paged_workspace_size")
 
 _lib = None
 
@@ -55,6 +58,16 @@ def mods(window_left: int = -1, window_right: int = -1, prefix: int = 0, doc_ids
     """An fa_mods value; doc_ids is an int32 CUDA tensor [N] or None."""
     return FaMods(int(window_left), int(window_right), int(prefix),
                   None if doc_ids is None else doc_ids.data_ptr(), float(softcap))
+
+
+class FaCache(ctypes.Structure):
+    """fa_cache of include/fa.h: a paged key/value cache."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("layer_stride", ctypes.c_longlong), ("page_stride", ctypes.c_longlong),
+                ("layers", ctypes.c_int), ("pages", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("seqs", ctypes.c_int), ("seq_pages", ctypes.c_int), ("err", ctypes.c_void_p)]
 
 
 class FaError(RuntimeError):
@@ -112,6 +125,23 @@ def lib() -> ctypes.CDLL:
         L.fa_debug_set_stall.restype = _I
         L.fa_bwd_varlen_workspace_size.argtypes = [_I, _I, _I, _I, _I]
         L.fa_bwd_varlen_workspace_size.restype = _S
+        C = ctypes.POINTER(FaCache)
+        for n, args in (("fa_cache_extend", [C, _P, _I, _P, _I, _P, _P, _S, _P]),
+                        ("fa_cache_write", [C, _I, _P, _P, _P, _P, _I, _P, _I, _P]),
+                        ("fa_cache_fork", [C, _P, _P, _I, _P, _S, _P]),
+                        ("fa_cache_free", [C, _P, _I, _P, _S, _P]),
+                        ("fa_cache_copy", [C, _P, _P, _I, _P, _S, _P]),
+                        ("fa_cache_compact", [C, _P, _S, _P]),
+                        ("fa_fwd_paged", [C, _I, _P, _P, _P, _P, _I, _I, _I, _F, _I, _I, _F, _P,
+                                          _S, _P]),
+                        ("fa_fwd_shared", [C, _I, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _F,
+                                           _P, _S, _P])):
+            getattr(L, n).argtypes = args
+            getattr(L, n).restype = _I
+        L.fa_cache_workspace_size.argtypes = [C, _I]
+        L.fa_cache_workspace_size.restype = _S
+        L.fa_paged_workspace_size.argtypes = [C, _I, _I, _I, _I]
+        L.fa_paged_workspace_size.restype = _S
         _lib = L
     return _lib
 
@@ -208,6 +238,46 @@ def fa_debug_set_stall(kernels: int, wait_cycles: int) -> int:
 
 def fa_bwd_varlen_workspace_size(B, Hq, max_seqlen, total, d) -> int:
     return lib().fa_bwd_varlen_workspace_size(B, Hq, max_seqlen, total, d)
+
+
+def fa_cache_workspace_size(cache, n) -> int:
+    return lib().fa_cache_workspace_size(cache, n)
+
+
+def fa_cache_extend(*args) -> int:
+    return lib().fa_cache_extend(*args)
+
+
+def fa_cache_write(*args) -> int:
+    return lib().fa_cache_write(*args)
+
+
+def fa_cache_fork(*args) -> int:
+    return lib().fa_cache_fork(*args)
+
+
+def fa_cache_free(*args) -> int:
+    return lib().fa_cache_free(*args)
+
+
+def fa_cache_copy(*args) -> int:
+    return lib().fa_cache_copy(*args)
+
+
+def fa_cache_compact(*args) -> int:
+    return lib().fa_cache_compact(*args)
+
+
+def fa_fwd_paged(*args) -> int:
+    return lib().fa_fwd_paged(*args)
+
+
+def fa_fwd_shared(*args) -> int:
+    return lib().fa_fwd_shared(*args)
+
+
+def fa_paged_workspace_size(cache, B, T, Hq, shared) -> int:
+    return lib().fa_paged_workspace_size(cache, B, T, Hq, shared)
 
 
 # ------------------------------------------------------------------ torch helpers
@@ -445,3 +515,209 @@ def attention(q, k, v, scale: Optional[float] = None, causal: bool = False, bloc
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     return _autograd_fn().apply(q, k, v, scale, causal, block_mask)
+
+
+# ------------------------------------------------------------------ paged cache
+
+class _on:
+    """Makes a tensor's device current, where it is not."""
+
+    def __init__(self, device):
+        import torch
+        self.to = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.to is not None:
+            self.to.__enter__()
+
+    def __exit__(self, *exc):
+        if self.to is not None:
+            self.to.__exit__(*exc)
+
+
+class PagedCache:
+    """Keys and values of many sequences in a pool of fixed-size pages (fa_cache
+    of include/fa.h, which says what the calls do and when they are refused).
+
+    k, v: [layers, pages, Hkv, page_size, d] CUDA tensors, bf16 or fp32, with
+    equal strides and contiguous pages; table int32 [seqs, seq_pages], lens int32
+    [seqs], refs int32 [pages], contiguous. The cache keeps and updates these
+    tensors; ``new`` makes an empty one. Lists of slots and pages are int32 CUDA
+    tensors. Calls are asynchronous on the current stream; what the device
+    refuses is raised by ``check``."""
+
+    def __init__(self, k, v, table, lens, refs):
+        import torch
+        if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise ValueError("k and v are [layers, pages, Hkv, page_size, d] of one type and stride")
+        L, P, Hkv, ps, d = k.shape
+        if min(k.shape) < 1 or k.stride()[2:] != (ps * d, d, 1):
+            raise ValueError("a page [Hkv, page_size, d] of k and v is contiguous and not empty")
+        if table.dim() != 2 or lens.shape != table.shape[:1] or refs.shape != (P,):
+            raise ValueError("table is [seqs, seq_pages], lens [seqs], refs [pages]")
+        for t in (table, lens, refs):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("table, lens and refs are contiguous int32 tensors")
+        if not k.is_cuda or any(t.device != k.device for t in (v, table, lens, refs)):
+            raise ValueError("the tensors of a cache are on one CUDA device")
+        self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
+        self.device, self.dtype = k.device, k.dtype
+        self.layers, self.pages, self.Hkv, self.page_size, self.d = k.shape
+        self.err = torch.zeros(64, dtype=torch.int32, device=k.device)
+        self._c = FaCache(_ptr(k), _ptr(v), k.stride(0), k.stride(1), L, P, Hkv, ps, d,
+                          _dtype_code(k.dtype), _ptr(table), _ptr(lens), _ptr(refs),
+                          table.shape[0], table.shape[1], _ptr(self.err))
+        self._ref = ctypes.byref(self._c)
+        if fa_cache_workspace_size(self._ref, 0) == 0:
+            raise ValueError("unsupported cache: page_size is 16, 32, 64 or 128, d 16, 32, 64 or "
+                             "128, strides are multiples of 16 bytes")
+
+    @classmethod
+    def new(cls, layers: int, pages: int, Hkv: int, page_size: int, d: int, seqs: int,
+            seq_pages: int, dtype=None, device="cuda"):
+        """An empty cache (dtype defaults to bfloat16)."""
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        shape = (layers, pages, Hkv, page_size, d)
+        k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        table = torch.full((seqs, seq_pages), -1, dtype=torch.int32, device=device)
+        lens, refs = (torch.zeros(n, dtype=torch.int32, device=device) for n in (seqs, pages))
+        return cls(k, v, table, lens, refs)
+
+    def _list(self, *tensors):
+        import torch
+        for t in tensors:
+            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+                    t.device != self.device:
+                raise ValueError("a list is a contiguous int32 tensor on the cache's device")
+            if t.numel() != tensors[0].numel():
+                raise ValueError("lists of different lengths")
+        return tensors[0].numel()
+
+    def _workspace(self, n: int):
+        import torch
+        return torch.empty(fa_cache_workspace_size(self._ref, n), dtype=torch.uint8,
+                           device=self.device)
+
+    def _stream(self):
+        import torch
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def extend(self, seqs, tokens):
+        """Makes room for new tokens: `tokens` of each sequence, or cu_seqlens
+        (int32 [n + 1]). Returns the positions of the first ones, int32 [n]."""
+        import torch
+        n = self._list(seqs)
+        cu = None
+        if not isinstance(tokens, int):
+            if self._list(tokens) != n + 1:
+                raise ValueError("cu_seqlens has one entry more than the list of sequences")
+            cu, tokens = tokens, 0
+        with _on(self.device):
+            pos = torch.empty_like(seqs)
+            ws = self._workspace(n)
+            _check(fa_cache_extend(self._ref, _ptr(seqs), n, _ptr(cu), tokens, _ptr(pos), _ptr(ws),
+                                   ws.numel(), self._stream()), "fa_cache_extend")
+        return pos
+
+    def write(self, layer: int, k, v, seqs, pos, cu_seqlens=None):
+        """Writes new keys and values [total, Hkv, d] of one layer from the
+        positions that extend returned on; rows of equal shares, or cu_seqlens."""
+        n = self._list(seqs, pos)
+        if cu_seqlens is not None and self._list(cu_seqlens) != n + 1:
+            raise ValueError("cu_seqlens has one entry more than the list of sequences")
+        for t in (k, v):
+            if t.dim() != 3 or t.shape[1:] != (self.Hkv, self.d) or t.dtype != self.dtype or \
+                    not t.is_contiguous() or t.device != self.device or t.shape != k.shape:
+                raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
+        with _on(self.device):
+            _check(fa_cache_write(self._ref, layer, _ptr(k), _ptr(v), _ptr(seqs), _ptr(pos), n,
+                                  _ptr(cu_seqlens), k.shape[0], self._stream()), "fa_cache_write")
+
+    def _op(self, name, fn, *lists):
+        n = self._list(*lists)
+        with _on(self.device):
+            ws = self._workspace(n)
+            _check(fn(self._ref, *map(_ptr, lists), n, _ptr(ws), ws.numel(), self._stream()), name)
+
+    def fork(self, src, dst):
+        """Makes the empty sequences dst copies of src: full pages are shared."""
+        self._op("fa_cache_fork", fa_cache_fork, src, dst)
+
+    def free(self, seqs):
+        """Empties sequences and gives up their pages."""
+        self._op("fa_cache_free", fa_cache_free, seqs)
+
+    def copy_pages(self, src, dst):
+        """Copies pages src to pages dst in all layers."""
+        self._op("fa_cache_copy", fa_cache_copy, src, dst)
+
+    def compact(self):
+        """Moves the pages in use to the front of the pool."""
+        with _on(self.device):
+            ws = self._workspace(0)
+            _check(fa_cache_compact(self._ref, _ptr(ws), ws.numel(), self._stream()),
+                   "fa_cache_compact")
+
+    def check(self):
+        """Raises FaError if the device refused a call since the last check
+        (synchronises the stream)."""
+        with _on(self.device):
+            _check(fa_get_device_error(_ptr(self.err), self._stream()), "paged cache")
+
+
+def _forward_cache(q, cache, layer, shared, seqs, scale, causal, window_left, softcap, out, lse,
+                   workspace):
+    import torch
+    if q.dim() != 4 or q.dtype != cache.dtype or q.device != cache.device or \
+            not q.is_contiguous() or q.shape[3] != cache.d:
+        raise ValueError("q is a contiguous [B, Hq, T, d] of the cache's type, on its device")
+    B, Hq, T, d = q.shape
+    if seqs is not None and cache._list(seqs) != B:
+        raise ValueError("one sequence for each batch entry")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or
+                            out.device != q.device or not out.is_contiguous()):
+        raise ValueError("out is like q")
+    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or
+                            lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError("lse is float32 [B, Hq, T]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(cache.device):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(fa_paged_workspace_size(cache._ref, B, T, Hq, shared),
+                             dtype=torch.uint8, device=q.device)
+        elif ws.device != q.device or not ws.is_contiguous():
+            raise ValueError("workspace is contiguous, on the cache's device")
+        nbytes = ws.numel() * ws.element_size()
+        if shared:
+            _check(fa_fwd_shared(cache._ref, layer, _ptr(q), _ptr(o), _ptr(l), _ptr(seqs), B, T,
+                                 Hq, shared, scale, int(bool(causal)), window_left, softcap,
+                                 _ptr(ws), nbytes, cache._stream()), "fa_fwd_shared")
+        else:
+            _check(fa_fwd_paged(cache._ref, layer, _ptr(q), _ptr(o), _ptr(l), _ptr(seqs), B, T, Hq,
+                                scale, int(bool(causal)), window_left, softcap, _ptr(ws), nbytes,
+                                cache._stream()), "fa_fwd_paged")
+    return o, l
+
+
+def forward_paged(q, cache: PagedCache, layer: int, seqs=None, scale: Optional[float] = None,
+                  causal: bool = True, window_left: int = -1, softcap: float = 0.0, out=None,
+                  lse=None, workspace=None):
+    """O, LSE of the last T tokens of each sequence over the cache (fa_fwd_paged).
+    q [B, Hq, T, d]; seqs int32 [B], or None for slots 0 .. B-1. A workspace
+    (fa_paged_workspace_size bytes) serves one call at a time."""
+    return _forward_cache(q, cache, layer, 0, seqs, scale, causal, window_left, softcap, out, lse,
+                          workspace)
+
+
+def forward_shared(q, cache: PagedCache, layer: int, shared: int, seqs=None,
+                   scale: Optional[float] = None, causal: bool = True, window_left: int = -1,
+                   softcap: float = 0.0, out=None, lse=None, workspace=None):
+    """forward_paged for sequences that begin with the same `shared` tokens (a
+    multiple of the page size), read once for the batch (fa_fwd_shared)."""
+    return _forward_cache(q, cache, layer, int(shared), seqs, scale, causal, window_left, softcap,
+                          out, lse, workspace)

@@ -61,7 +61,8 @@ typedef enum {
   FA_ERR_INVALID_ARG = 1,
   FA_ERR_UNSUPPORTED = 2,
   FA_ERR_CUDA = 3,
-  FA_ERR_TIMEOUT = 4
+  FA_ERR_TIMEOUT = 4,
+  FA_ERR_CACHE = 5 /* a cache operation was refused on the device (fa_cache, below) */
 } fa_status;
 
 /* Element types of Q, K, V, O, dO (dtype) and of dQ, dK, dV (grad_dtype). */
@@ -360,6 +361,140 @@ fa_status fa_exp2_fma(const float* x, float* y, long long n, void* stream);
 enum { FA_STALL_FWD = 1, FA_STALL_BWD = 2, FA_STALL_DQ = 4 };
 fa_status fa_debug_set_stall(int kernels, long long wait_cycles);
 
+/*
+ * Paged key/value cache: the keys and values of many sequences in one pool of
+ * fixed-size pages, for answering token by token (the pages have no
+ * counterpart: they describe training-shaped attention, whose K and V these
+ * entry points keep between calls). A cache holds
+ *   K, V    [layers][pages][Hkv][page_size][d] (dtype), device;
+ *   table   int32 [seqs][seq_pages]: token i of the sequence in slot s lies in
+ *           row i % page_size of page table[s][i / page_size]; -1 behind the
+ *           sequence's last page;
+ *   lens    int32 [seqs]: tokens of each slot, 0 for an empty one;
+ *   refs    int32 [pages]: how many tables hold a page; 0 = free;
+ *   err     one device word, zeroed once: fa_get_device_error reads it.
+ * An empty cache has table = -1, lens = 0, refs = 0. The caller owns all of
+ * it; everything is updated on `stream`, with no host copy, so a decoding
+ * step can be captured into a CUDA graph. Calls that change one cache must be
+ * ordered by the caller.
+ *
+ * Strides are in elements: layer_stride between layers, page_stride between
+ * the pages of a layer (multiples of 16 bytes; within a page the layout is
+ * contiguous), so K and V may be two halves of one tensor or the layers may
+ * lie inside the pages. K, V 16-byte aligned; the int32 arrays 4-byte.
+ * page_size in {16, 32, 64, 128}, d in {16, 32, 64, 128}, dtype FA_F32 or
+ * FA_BF16; K and V may exceed 2^31 elements.
+ *
+ * What the device finds wrong in lists of slots and pages (a slot or page out
+ * of range, one named twice, no free page left, a sequence past seq_pages
+ * pages, a destination in use) refuses the WHOLE call: the cache stays as it
+ * was, and err gets a bit that fa_get_device_error(err, stream) reports as
+ * FA_ERR_CACHE and clears. New pages are always the lowest free ones, in the
+ * order of the call's list, so results never depend on timing.
+ */
+typedef struct {
+  void* K;
+  void* V;
+  long long layer_stride;
+  long long page_stride;
+  int layers, pages, Hkv, page_size, d, dtype;
+  int* table;
+  int* lens;
+  int* refs;
+  int seqs, seq_pages;
+  unsigned* err;
+} fa_cache;
+
+/* Workspace of the fa_cache_* calls below for lists of n entries (device, 16-byte
+ * aligned, no initial value; it serves one call at a time). 0 for a bad cache. */
+size_t fa_cache_workspace_size(const fa_cache* cache, int n);
+
+/*
+ * Makes room for new tokens behind n sequences: lens[seqs[i]] grows by `tokens`
+ * (cu_seqlens == NULL), or by cu_seqlens[i + 1] - cu_seqlens[i] (device int32
+ * [n + 1]), and pages are taken as needed. pos[i] (device int32 [n]) gets the old length,
+ * the position of the first new token, or -1 when the call is refused.
+ */
+fa_status fa_cache_extend(const fa_cache* cache, const int* seqs, int n, const int* cu_seqlens,
+                          int tokens, int* pos, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Writes K and V of `total` tokens ([total][Hkv][d], contiguous, 16-byte
+ * aligned) into one layer: token j of sequence i, row cu_seqlens[i] + j (row
+ * i * (total / n) + j without cu_seqlens), goes to position pos[i] + j. Rows of
+ * a sequence with pos < 0 are skipped. A position behind the sequence's length, or in a page
+ * that more than one table holds, is not written and reported as FA_ERR_CACHE.
+ * No workspace.
+ */
+fa_status fa_cache_write(const fa_cache* cache, int layer, const void* K, const void* V,
+                         const int* seqs, const int* pos, int n, const int* cu_seqlens,
+                         int total, void* stream);
+
+/*
+ * dst[i] becomes a copy of src[i], i < n: it shares src's full pages (their
+ * refs grow) and gets a page of its own, copied in all layers, for a partly
+ * filled last one, so both can grow on. The dst slots must be empty, distinct and no
+ * src; a src may occur many times.
+ */
+fa_status fa_cache_fork(const fa_cache* cache, const int* src, const int* dst, int n,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Empties n distinct slots: each page's refs shrink, and a page at 0 is free. */
+fa_status fa_cache_free(const fa_cache* cache, const int* seqs, int n, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Copies page src[i] to page dst[i] in all layers, i < n. Tables and refs stay.
+ * The dst pages must be distinct and no src of the call.
+ */
+fa_status fa_cache_copy(const fa_cache* cache, const int* src, const int* dst, int n,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves the pages in use to the front of the pool: of L pages with refs > 0,
+ * those at L or behind move, in order, into the free pages below L, in order;
+ * tables and refs follow. Afterwards the pages L .. pages-1 are free.
+ */
+fa_status fa_cache_compact(const fa_cache* cache, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * Attention of the last T tokens of B sequences over one layer of the cache:
+ * Q, O [B][Hq][T][d] (the cache's dtype), LSE float [B][Hq][T]. Query t of the
+ * sequence in slot seqs[b] (slot b when seqs == NULL) has position
+ * i = len - T + t and sees key j < len iff
+ *   (causal == 0 or j <= i) and (window_left < 0 or j >= i - window_left);
+ * softcap > 0 caps the scores as in fa_mods. A query that sees no key (an
+ * empty slot, i < 0, seqs[b] out of range) gets O = 0 and LSE = -inf. K and V
+ * rows that no query of the call sees may hold anything. A non-finite V row
+ * may spread to every query of a call that sees a key in the 128-key
+ * neighbourhood. Table entries out of range read page 0.
+ * workspace: fa_paged_workspace_size bytes, device, 16-byte aligned, no
+ * initial value; one call at a time. A bounded wait that runs out is reported
+ * through cache->err (FA_ERR_TIMEOUT). Deterministic.
+ */
+fa_status fa_fwd_paged(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
+                       const int* seqs, int B, int T, int Hq, float scale, int causal,
+                       int window_left, float softcap, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * fa_fwd_paged for sequences that begin with the same `shared` tokens (a
+ * multiple of page_size; e.g. forks of one prompt): their keys and values are
+ * read through the table of the FIRST sequence, once for the whole batch, and
+ * each sequence's own table from token `shared` on. Results are those of
+ * fa_fwd_paged when the tables agree up to there. A sequence shorter than
+ * `shared` sees its length of them.
+ */
+fa_status fa_fwd_shared(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
+                        const int* seqs, int B, int T, int Hq, int shared, float scale,
+                        int causal, int window_left, float softcap, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace of fa_fwd_paged (shared = 0) and fa_fwd_shared. 0 for bad sizes. */
+size_t fa_paged_workspace_size(const fa_cache* cache, int B, int T, int Hq, int shared);
+
 /* Number of kernel launches the last successful call of fa_fwd_ex / fa_bwd_ex
  * or one of the stages made from the calling thread (for launch accounting). */
 int fa_last_launch_count(void);
@@ -367,7 +502,8 @@ int fa_last_launch_count(void);
 /*
  * Reads and clears the workspace's error word: synchronises `stream`, copies
  * the word to the host, then zeroes it. Returns FA_OK if no kernel recorded a
- * failure, FA_ERR_TIMEOUT if a bounded wait ran out, FA_ERR_CUDA if the copy
+ * failure, FA_ERR_TIMEOUT if a bounded wait ran out, FA_ERR_CACHE if a cache
+ * operation was refused (`workspace` is then the cache's err), FA_ERR_CUDA if the copy
  * failed (and then leaves the word as it is).
  */
 fa_status fa_get_device_error(void* workspace, void* stream);
