@@ -71,6 +71,9 @@ struct PagedArgs {
 
 // Kernel families. Each runs one phase (`pre`: the shared prefix).
 cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
+// mma.sync kernel for up to kMmaMaxRows packed rows an item (bf16, d in {64, 128}).
+constexpr int kMmaTile = 32, kMmaMaxRows = 32;
+cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
 // Joins the partial results of both phases.
 cudaError_t paged_join(const PagedArgs& a, int dtype, cudaStream_t st);
 

@@ -84,23 +84,30 @@ int sm_count() {
 // Blocks of the CUDA-core kernel per SM, its rows and keys per tile.
 constexpr int kSimtPerSm = 4, kSimtRows = 8, kSimtTile = 32;
 
-// The work division of a call. It depends on sizes only, so the workspace query
-// and the call agree.
-void plan(PagedArgs& a, int sms) {
-  const int R = a.B * a.TG;
-  a.own.rows = kSimtRows;
-  a.own.tile = kSimtTile;
-  a.own.rt = (a.TG + kSimtRows - 1) / kSimtRows;
-  a.own.items = a.B * a.c.Hkv * a.own.rt;
-  a.own.n = sms * kSimtPerSm;
-  a.pre = Phase();
-  a.pre.rows = kSimtRows;
-  a.pre.tile = kSimtTile;
-  if (a.shared) {
-    a.pre.rt = (R + kSimtRows - 1) / kSimtRows;
-    a.pre.items = a.c.Hkv * a.pre.rt;
-    a.pre.n = sms * kSimtPerSm;
+// The work division of a phase of `heads` row groups with `rows` packed rows each. It
+// depends on sizes and types only, so the workspace query and the call agree.
+// bf16 with d of 64 or 128 runs on the tensor cores, all else on the CUDA cores.
+bool on_mma(const CacheView& v) { return v.row_bytes == 2 * v.d && v.d >= 64; }
+
+Phase divide(const CacheView& v, int groups, int rows, int sms) {
+  Phase p;
+  if (on_mma(v)) {
+    p.rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : kMmaMaxRows);
+    p.tile = kMmaTile;
+    p.n = sms;
+  } else {
+    p.rows = kSimtRows;
+    p.tile = kSimtTile;
+    p.n = sms * kSimtPerSm;
   }
+  p.rt = (rows + p.rows - 1) / p.rows;
+  p.items = groups * p.rt;
+  return p;
+}
+
+void plan(PagedArgs& a, int sms) {
+  a.own = divide(a.c, a.B * a.c.Hkv, a.TG, sms);
+  a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, sms) : Phase();
 }
 
 size_t phase_bytes(const Phase& p, int d, size_t* lse_at) {
@@ -166,9 +173,11 @@ fa_status fwd(const fa_cache* cache, int layer, const void* Q, void* O, float* L
   a.pre.o = reinterpret_cast<float*>(w + own);
   a.pre.lse = reinterpret_cast<float*>(w + own + pre_lse);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (shared)
-    if (cudaError_t e = paged_simt(a, true, cache->dtype, st)) return from_cuda(e);
-  if (cudaError_t e = paged_simt(a, false, cache->dtype, st)) return from_cuda(e);
+  for (int pre = shared ? 1 : 0; pre >= 0; --pre) {
+    const cudaError_t e =
+        on_mma(v) ? paged_mma(a, pre != 0, st) : paged_simt(a, pre != 0, cache->dtype, st);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
   return from_cuda(paged_join(a, cache->dtype, st));
 }
 

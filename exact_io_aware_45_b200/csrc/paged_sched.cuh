@@ -45,11 +45,13 @@ __device__ __forceinline__ int tiles_of(int lo, int hi, int tile) {
   return hi > lo ? (hi - 1) / tile - lo / tile + 1 : 1;
 }
 
-// Keys [lo, hi) of the shared phase, from the smallest length of the batch.
-__device__ __forceinline__ void pre_keys(const PagedArgs& a, int min_len, int& lo, int& hi) {
+// Keys [lo, hi) that any query sees of the shared prefix, from the smallest and
+// the largest length of the batch.
+__device__ __forceinline__ void pre_keys(const PagedArgs& a, int least, int most, int& lo,
+                                         int& hi) {
   lo = 0;
-  hi = a.shared;
-  if (a.wl >= 0) lo = max(0ll, min((long long)a.shared, (long long)min_len - a.T - a.wl));
+  hi = min(a.shared, most);
+  if (a.wl >= 0) lo = max(0ll, min((long long)hi, (long long)least - a.T - a.wl));
 }
 
 // CTAs that take part, and the raw cut of CTA i.
@@ -102,7 +104,7 @@ struct Scratch {
   long long warp[32];
   long long cut[2], start[2];
   int cut_b[2];
-  int warp_min[32];
+  int least[32], most[32];
 };
 
 // Finds this CTA's tiles [w.x, end) and sets up the walk; all `threads` threads
@@ -114,10 +116,11 @@ __device__ inline bool begin(const PagedArgs& a, const Phase& ph, bool pre, int 
   const int per = (a.B + threads - 1) / threads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long sum = 0;
-  int least = 0x7fffffff;
+  int least = 0x7fffffff, most = 0;
   for (int b = b0; b < b1; ++b) {
     const int len = len_of(a, b);
     least = min(least, len);
+    most = max(most, len);
     int lo, hi;
     own_keys(a, len, lo, hi);
     sum += (long long)tiles_of(lo, hi, ph.tile) * per_b;
@@ -129,18 +132,20 @@ __device__ inline bool begin(const PagedArgs& a, const Phase& ph, bool pre, int 
     if (lane >= o) x += y;
   }
   least = __reduce_min_sync(~0u, least);
-  if (lane == 31) s.warp[wid] = x, s.warp_min[wid] = least;
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 31) s.warp[wid] = x, s.least[wid] = least, s.most[wid] = most;
   __syncthreads();
   long long before = 0, W = 0;
   for (int i = 0; i < warps; ++i) {
     if (i < wid) before += s.warp[i];
     W += s.warp[i];
-    least = min(least, s.warp_min[i]);
+    least = min(least, s.least[i]);
+    most = max(most, s.most[i]);
   }
   before += x - sum;
   if (pre) {
     int lo, hi;
-    pre_keys(a, least, lo, hi);
+    pre_keys(a, least, most, lo, hi);
     const int nt = tiles_of(lo, hi, ph.tile);
     W = (long long)ph.items * nt;
     const int n = ctas_of(ph.n, W);

@@ -244,12 +244,12 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
   __shared__ long long part[kJoinWarps][2];
-  __shared__ int least_of[kJoinWarps];
+  __shared__ int least_of[kJoinWarps], most_of[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x - b * a.c.Hkv;
   const int per_b = a.c.Hkv * a.own.rt;
   long long before = 0, W = 0;
-  int least = 0x7fffffff;
+  int least = 0x7fffffff, most = 0;
   for (int i = tid; i < a.B; i += kJoinWarps * 32) {
     const int len = sched::len_of(a, i);
     int lo, hi;
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
     W += t;
     if (i < b) before += t;
     least = min(least, len);
+    most = max(most, len);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -265,18 +266,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
     W += __shfl_xor_sync(~0u, W, o);
   }
   least = __reduce_min_sync(~0u, least);
-  if (lane == 0) part[warp][0] = before, part[warp][1] = W, least_of[warp] = least;
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 0) {
+    part[warp][0] = before, part[warp][1] = W;
+    least_of[warp] = least, most_of[warp] = most;
+  }
   __syncthreads();
   before = W = 0;
   for (int i = 0; i < kJoinWarps; ++i) {
     before += part[i][0], W += part[i][1];
     least = min(least, least_of[i]);
+    most = max(most, most_of[i]);
   }
   int lo, hi;
   sched::own_keys(a, sched::len_of(a, b), lo, hi);
   const int nt = sched::tiles_of(lo, hi, a.own.tile);
   const int n = sched::ctas_of(a.own.n, W);
-  sched::pre_keys(a, least, lo, hi);
+  sched::pre_keys(a, least, most, lo, hi);
   const int pre_nt = a.shared ? sched::tiles_of(lo, hi, a.pre.tile) : 0;
   const long long pre_W = (long long)a.pre.items * pre_nt;
   const int pre_n = a.shared ? sched::ctas_of(a.pre.n, pre_W) : 0;
