@@ -41,17 +41,23 @@ cudaError_t cache_compact(const CacheView& c, void* ws, cudaStream_t st);
 size_t cache_workspace_bytes(int pages, int slots, int n);
 
 // One phase of an attention call: `items` row tiles (of up to `rows` packed
-// query rows that share a KV head), each over its own key tiles of `tile` keys,
-// laid end to end and cut into `n` even ranges, one per CTA.
+// query rows that share a KV head), each over its own key tiles of `tile` keys, cut
+// into even ranges for `n` streams (paged_sched.cuh).
 struct Phase {
   int rows = 0;        // query rows per item, at most
   int tile = 0;        // keys per tile
   int rt = 0;          // row tiles per (sequence, KV head); per KV head in the shared phase
-  int n = 0;           // CTAs
+  int n = 0;           // streams
   int items = 0;
   float* o = nullptr;  // partial results: [items + n][rows][d], normalised
   float* lse = nullptr;  // [items + n][rows], base 2
 };
+
+namespace sched {
+// Units of an item beside its tiles, tiles that a cut keeps from an item's ends,
+// and units that a stream is worth.
+constexpr int kOver = 4, kSnap = 4, kMinUnits = 12;
+}  // namespace sched
 
 struct PagedArgs {
   CacheView c;
@@ -71,9 +77,11 @@ struct PagedArgs {
 
 // Kernel families. Each runs one phase (`pre`: the shared prefix).
 cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
-// mma.sync kernel for up to kMmaMaxRows packed rows an item (bf16, d in {64, 128}).
-constexpr int kMmaTile = 32, kMmaMaxRows = 32;
+constexpr int kSimtRows = 8, kSimtTile = 32, kSimtBlocksPerSm = 4;
+// mma.sync kernel for few packed rows (bf16, d in {64, 128}); a stream is a warp.
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
+constexpr int kMmaMaxRows = 16, kMmaWarps = 8;
+constexpr int mma_tile(int d) { return d == 128 ? 16 : 32; }
 // Joins the partial results of both phases.
 cudaError_t paged_join(const PagedArgs& a, int dtype, cudaStream_t st);
 

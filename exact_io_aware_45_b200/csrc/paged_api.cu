@@ -81,33 +81,36 @@ int sm_count() {
   return n;
 }
 
-// Blocks of the CUDA-core kernel per SM, its rows and keys per tile.
-constexpr int kSimtPerSm = 4, kSimtRows = 8, kSimtTile = 32;
-
-// The work division of a phase of `heads` row groups with `rows` packed rows each. It
-// depends on sizes and types only, so the workspace query and the call agree.
-// bf16 with d of 64 or 128 runs on the tensor cores, all else on the CUDA cores.
+// The work division of a phase of `groups` sequences and KV heads with `rows`
+// packed rows each. It depends on sizes and types only, so the workspace query
+// and the call agree. bf16 with d of 64 or 128 runs on the tensor cores, all
+// else on the CUDA cores.
 bool on_mma(const CacheView& v) { return v.row_bytes == 2 * v.d && v.d >= 64; }
 
 Phase divide(const CacheView& v, int groups, int rows, int sms) {
   Phase p;
   if (on_mma(v)) {
-    p.rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : kMmaMaxRows);
-    p.tile = kMmaTile;
-    p.n = sms;
+    p.rows = rows <= 8 ? 8 : kMmaMaxRows;
+    p.tile = mma_tile(v.d);
+    p.n = sms * kMmaWarps;
   } else {
     p.rows = kSimtRows;
     p.tile = kSimtTile;
-    p.n = sms * kSimtPerSm;
+    p.n = sms * kSimtBlocksPerSm;
   }
   p.rt = (rows + p.rows - 1) / p.rows;
   p.items = groups * p.rt;
   return p;
 }
 
-void plan(PagedArgs& a, int sms) {
+// Fills in both phases; false if their units do not fit an int.
+bool plan(PagedArgs& a, int sms) {
   a.own = divide(a.c, a.B * a.c.Hkv, a.TG, sms);
   a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, sms) : Phase();
+  const long long keys = (long long)a.c.width << a.c.page_log2;
+  const long long most = keys / a.own.tile + 2 + sched::kOver;
+  return a.own.items * most < (1ll << 31) - (1 << 20) &&
+         a.pre.items * most < (1ll << 31) - (1 << 20);
 }
 
 size_t phase_bytes(const Phase& p, int d, size_t* lse_at) {
@@ -163,7 +166,7 @@ fa_status fwd(const fa_cache* cache, int layer, const void* Q, void* O, float* L
   a.wl = window_left;
   a.scale = scale;
   a.softcap = softcap;
-  plan(a, sm_count());
+  if (!plan(a, sm_count())) return FA_ERR_UNSUPPORTED;
   size_t own_lse, pre_lse;
   const size_t own = phase_bytes(a.own, v.d, &own_lse), pre = phase_bytes(a.pre, v.d, &pre_lse);
   if (!ws || !aligned(ws, 16) || ws_bytes < own + pre) return FA_ERR_INVALID_ARG;
@@ -272,7 +275,7 @@ size_t fa_paged_workspace_size(const fa_cache* cache, int B, int T, int Hq, int 
   if (view_of(cache, v) != FA_OK || check_fwd(v, B, T, Hq, shared) != FA_OK) return 0;
   PagedArgs a;
   sizes(a, v, B, T, Hq, shared);
-  plan(a, sm_count());
+  if (!plan(a, sm_count())) return 0;
   size_t at;
   return phase_bytes(a.own, v.d, &at) + phase_bytes(a.pre, v.d, &at);
 }

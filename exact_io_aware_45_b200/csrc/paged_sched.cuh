@@ -2,16 +2,20 @@
 // compute partial results and the kernel that joins them.
 //
 // A phase's items (row tiles of packed query rows over one key range) are laid
-// end to end as W key tiles. CTA i of n takes tiles [x_i, x_{i+1}), x_i = i W / n:
-// the load is even whatever the lengths are, and no length has to be known on
-// the host. A cut closer than kSnap tiles to an item's end moves to that end,
-// which spares partial results of a few tiles; n shrinks to W / kMinTiles for
-// little work.
+// end to end as W units: kOver for an item's set-up and result, then one for each
+// key tile. Stream i of n (a warp, or a block) takes units [x_i, x_{i+1}), all
+// streams as even as whole units allow: the load does not depend on how the
+// lengths are spread, and no length has to be known on the host. A cut in an item's first
+// kOver units or closer than kSnap tiles to either end moves to that end, which
+// spares partial results of a few tiles; n shrinks to W / kMinUnits for little work.
 //
-// An item that one CTA covers whole and that no other phase adds to is written
+// An item that one stream covers whole and that no other phase adds to is written
 // to O and LSE directly. Otherwise each of its pieces goes to a slot of its
 // own: the piece with the item's first tile to slot `item`, a piece that begins
-// at CTA i's first tile to slot items + i.
+// with stream i's first tile to slot items + i.
+//
+// The packed rows of a sequence and KV head are (g, t), t fastest: contiguous in Q
+// and O. Units fit an int (checked on the host).
 #pragma once
 
 #include "paged.h"
@@ -19,30 +23,34 @@
 namespace fa {
 namespace sched {
 
-constexpr int kSnap = 4;
-constexpr int kMinTiles = 8;
-
 // Length of sequence b of the batch: 0 for a slot out of range.
 __device__ __forceinline__ int slot_of(const PagedArgs& a, int b) {
-  return a.seqs ? a.seqs[b] : b;
+  return a.seqs ? __ldg(a.seqs + b) : b;
+}
+__device__ __forceinline__ int len_at(const PagedArgs& a, int s) {
+  if ((unsigned)s >= (unsigned)a.c.slots) return 0;
+  return max(0, min(__ldg(a.c.lens + s), a.c.width << a.c.page_log2));
 }
 __device__ __forceinline__ int len_of(const PagedArgs& a, int b) {
-  const int s = slot_of(a, b);
-  if ((unsigned)s >= (unsigned)a.c.slots) return 0;
-  return max(0, min(a.c.lens[s], a.c.width << a.c.page_log2));
+  return len_at(a, slot_of(a, b));
 }
 
-// Keys [lo, hi) of sequence b that its queries can see behind the shared prefix
-// (own phase), and its number of key tiles: at least one, so that every item
-// has a CTA that writes its result.
+// Keys [lo, hi) of a sequence that its queries can see behind the shared prefix
+// (own phase), and units of an item over them: one tile at least, so that every
+// item has a stream that writes its result.
 __device__ __forceinline__ void own_keys(const PagedArgs& a, int len, int& lo, int& hi) {
   hi = len;
   lo = a.shared;
   // the window bound of the first query; in 64 bits, wl may be any int
   if (a.wl >= 0) lo = max((long long)lo, (long long)len - a.T - a.wl);
 }
-__device__ __forceinline__ int tiles_of(int lo, int hi, int tile) {
-  return hi > lo ? (hi - 1) / tile - lo / tile + 1 : 1;
+__device__ __forceinline__ int units_of(int lo, int hi, int tile) {
+  return kOver + (hi > lo ? (hi - 1) / tile - lo / tile + 1 : 1);
+}
+__device__ __forceinline__ int own_units(const PagedArgs& a, int len) {
+  int lo, hi;
+  own_keys(a, len, lo, hi);
+  return units_of(lo, hi, a.own.tile);
 }
 
 // Keys [lo, hi) that any query sees of the shared prefix, from the smallest and
@@ -54,240 +62,247 @@ __device__ __forceinline__ void pre_keys(const PagedArgs& a, int least, int most
   if (a.wl >= 0) lo = max(0ll, min((long long)hi, (long long)least - a.T - a.wl));
 }
 
-// CTAs that take part, and the raw cut of CTA i.
-__device__ __forceinline__ int ctas_of(int n, long long W) {
-  return (int)max(1ll, min((long long)n, W / kMinTiles));
-}
-__device__ __forceinline__ long long raw_cut(int i, long long W, int n) { return i * W / n; }
+// W units in n even ranges: the first `extra` are one longer.
+struct Cuts {
+  int W, n, each, extra;
+  __device__ Cuts(int units, int streams) : W(units) {
+    n = max(1, min(streams, W / kMinUnits));
+    each = W / n;
+    extra = W - each * n;
+  }
+  __device__ int at(int i) const { return i * each + min(i, extra); }
+  // the first cut at x or behind, and the last cut at x or before
+  __device__ int first(int x) const {
+    const int y = x - extra * (each + 1);
+    return y <= 0 ? (x + each) / (each + 1) : extra + (y + each - 1) / each;
+  }
+  __device__ int last(int x) const {
+    const int y = x - extra * (each + 1);
+    return y < 0 ? x / (each + 1) : extra + y / each;
+  }
+};
 
-// The cut x, moved to an end of its item [s, s + nt) when it lies close to one.
-__device__ __forceinline__ long long snap(long long x, long long s, int nt) {
-  if (x - s < kSnap) return s;
-  if (s + nt - x < kSnap) return s + nt;
+// The cut x, moved to an end of its item [s, s + u) when it lies close to one.
+__device__ __forceinline__ int snap(int x, int s, int u) {
+  if (x - s < kOver + kSnap) return s;
+  if (s + u - x < kSnap) return s + u;
   return x;
 }
 
-// Pieces of the item [s, s + nt): CTAs first + 1 .. first + more begin inside it.
-__device__ __forceinline__ void pieces_of(long long s, int nt, long long W, int n, int& first,
-                                          int& more) {
-  more = 0;
-  first = 0;
-  if (nt < 2 * kSnap) return;
-  const long long a = s + kSnap, b = s + nt - kSnap;   // cuts in [a, b] stay inside
-  first = (int)((a * n + W - 1) / W) - 1;              // floor(i W / n) >= a from first + 1 on
-  more = max(0, (int)(((b + 1) * n + W - 1) / W) - 1 - first);   // ... and <= b up to there
+// Pieces of the item [s, s + u): streams first + 1 .. first + more begin inside it.
+__device__ __forceinline__ void pieces_of(int s, int u, const Cuts& c, int& first, int& more) {
+  const int a = s + kOver + kSnap, b = s + u - kSnap;   // cuts in [a, b] stay inside
+  first = more = 0;
+  if (b < a) return;
+  first = c.first(a) - 1;
+  more = max(0, c.last(b) - first);
 }
 
-// Where a walk over a CTA's tiles stands.
-struct Walk {
-  long long x;       // next tile
-  long long s;       // first tile of the current item
-  int b;             // sequence (own phase), 0 in the shared phase
-  int item;          // (b * Hkv + h) * rt + row tile; (h * rt + row tile) in the shared phase
-  int h, r;          // KV head and row tile
-  int lo, hi;        // keys of the item
-  int nt;            // tiles of the item
-  int len;           // length of sequence b
+// The batch as one warp sees it: units of all sequences, those before sequence
+// `b`, the smallest and the largest length. All lanes call it.
+struct Batch {
+  int W, before, least, most;
 };
+__device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
+  Batch t{0, 0, 0x7fffffff, 0};
+  const int per_b = a.c.Hkv * a.own.rt;
+  for (int i = threadIdx.x & 31; i < a.B; i += 32) {
+    const int len = len_of(a, i);
+    const int u = own_units(a, len) * per_b;
+    t.W += u;
+    if (i < b) t.before += u;
+    t.least = min(t.least, len);
+    t.most = max(t.most, len);
+  }
+  t.W = __reduce_add_sync(~0u, t.W);
+  t.before = __reduce_add_sync(~0u, t.before);
+  t.least = __reduce_min_sync(~0u, t.least);
+  t.most = __reduce_max_sync(~0u, t.most);
+  return t;
+}
+
+// A stream's way through its units.
+struct Walk {
+  int x, end;        // next unit, and the first that is not its own
+  int s, u;          // first unit and units of the current item
+  int item;          // (b * Hkv + h) * rt + row tile; (h * rt + row tile) in the shared phase
+  int b, h, r;       // sequence (own phase), KV head, row tile
+  int lo, hi;        // keys of the item
+  int slot, len;     // of sequence b; the first sequence's slot in the shared phase
+  int slot1, len1;   // of the next sequence, and the slot after it: loaded ahead, since a
+  int slot2;         // chain of loads per sequence would stall short ones
+};
+
+__device__ __forceinline__ int slot_ahead(const PagedArgs& a, int b) {
+  return b < a.B ? slot_of(a, b) : -1;
+}
+__device__ __forceinline__ void enter(const PagedArgs& a, int b, Walk& w) {
+  w.b = b;
+  w.slot = slot_of(a, b);
+  w.slot1 = slot_ahead(a, b + 1);
+  w.slot2 = slot_ahead(a, b + 2);
+  w.len = len_at(a, w.slot);
+  w.len1 = len_at(a, w.slot1);
+  own_keys(a, w.len, w.lo, w.hi);
+  w.u = units_of(w.lo, w.hi, a.own.tile);
+}
+__device__ __forceinline__ void advance(const PagedArgs& a, Walk& w) {
+  ++w.b;
+  w.slot = w.slot1;
+  w.len = w.len1;
+  w.slot1 = w.slot2;
+  w.len1 = len_at(a, w.slot1);
+  w.slot2 = slot_ahead(a, w.b + 2);
+  own_keys(a, w.len, w.lo, w.hi);
+  w.u = units_of(w.lo, w.hi, a.own.tile);
+}
+
+// Sets up the walk of stream `i`; all lanes of a warp call it and get the same.
+// Returns false if the stream has no units.
+__device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
+  const int lane = threadIdx.x & 31;
+  const Batch t = scan_batch(a, 0);
+  if (pre) {
+    pre_keys(a, t.least, t.most, w.lo, w.hi);
+    w.u = units_of(w.lo, w.hi, a.pre.tile);
+    const Cuts c(a.pre.items * w.u, a.pre.n);
+    if (i >= c.n) return false;
+    const int x0 = c.at(i), x1 = c.at(i + 1);
+    w.item = x0 / w.u;
+    w.x = snap(x0, w.item * w.u, w.u);
+    w.end = x1 == c.W ? c.W : snap(x1, x1 / w.u * w.u, w.u);
+    if (w.x >= w.end) return false;
+    if (w.x >= (w.item + 1) * w.u) ++w.item;
+    w.s = w.item * w.u;
+    w.h = w.item / a.pre.rt;
+    w.r = w.item - w.h * a.pre.rt;
+    w.b = w.len = 0;
+    w.slot = slot_of(a, 0);
+    return true;
+  }
+  const Cuts c(t.W, a.own.n);
+  if (i >= c.n) return false;
+  const int per_b = a.c.Hkv * a.own.rt;
+  const int x0 = c.at(i), x1 = c.at(i + 1);
+  int at0 = 0, b0 = -1, base = 0;
+  w.end = x1 == c.W ? c.W : -1;
+  for (int g = 0; g < a.B && (b0 < 0 || w.end < 0); g += 32) {
+    const int u = g + lane < a.B ? own_units(a, len_of(a, g + lane)) : 0;
+    int to = u * per_b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, to, o);
+      if (lane >= o) to += y;
+    }
+    to += base;                                   // units up to and with this sequence
+    const int from = to - u * per_b;
+    const unsigned has0 = __ballot_sync(~0u, x0 >= from && x0 < to);
+    const unsigned has1 = __ballot_sync(~0u, x1 >= from && x1 < to);
+    if (has0) {
+      const int k = __ffs(has0) - 1;
+      b0 = g + k;
+      at0 = __shfl_sync(~0u, from, k);
+      const int v = __shfl_sync(~0u, u, k);
+      w.x = snap(x0, at0 + (x0 - at0) / v * v, v);
+    }
+    if (has1) {
+      const int k = __ffs(has1) - 1;
+      const int f = __shfl_sync(~0u, from, k), v = __shfl_sync(~0u, u, k);
+      w.end = snap(x1, f + (x1 - f) / v * v, v);
+    }
+    base = __shfl_sync(~0u, to, 31);
+  }
+  if (w.x >= w.end) return false;
+  enter(a, b0, w);
+  if (w.x >= at0 + w.u * per_b) {                 // moved to the next sequence's first unit
+    at0 += w.u * per_b;
+    advance(a, w);
+  }
+  const int in = (w.x - at0) / w.u;
+  w.s = at0 + in * w.u;
+  w.h = in / a.own.rt;
+  w.r = in - w.h * a.own.rt;
+  w.item = w.b * per_b + in;
+  return true;
+}
 
 // One piece of an item.
 struct Piece {
-  int h, b;          // KV head; sequence whose table names the keys
-  int row0, rows;    // packed query rows ((b * T + t) * G + g)
+  int h;             // KV head
+  int b, len;        // sequence and its length (own phase)
+  int table;         // slot whose table names the keys (the first sequence's in the shared phase)
+  int row0, rows;    // rows: (g, t) of sequence b, or (b, g, t) in the shared phase
   int lo, hi;        // keys in sight of any row
   int t0, t1;        // key tiles [t0, t1), in units of `tile` keys from key 0
   int slot;          // partial slot, or -1: write the result
 };
 
-// Per-block scratch of begin().
-struct Scratch {
-  long long warp[32];
-  long long cut[2], start[2];
-  int cut_b[2];
-  int least[32], most[32];
-};
-
-// Finds this CTA's tiles [w.x, end) and sets up the walk; all `threads` threads
-// of the block call it. Returns false if the CTA has none. Contains block barriers.
-__device__ inline bool begin(const PagedArgs& a, const Phase& ph, bool pre, int cta, int threads,
-                             Scratch& s, Walk& w, long long& end) {
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, warps = threads >> 5;
-  const int per_b = pre ? 0 : a.c.Hkv * ph.rt;
-  const int per = (a.B + threads - 1) / threads;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  long long sum = 0;
-  int least = 0x7fffffff, most = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int len = len_of(a, b);
-    least = min(least, len);
-    most = max(most, len);
-    int lo, hi;
-    own_keys(a, len, lo, hi);
-    sum += (long long)tiles_of(lo, hi, ph.tile) * per_b;
-  }
-  long long x = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += y;
-  }
-  least = __reduce_min_sync(~0u, least);
-  most = __reduce_max_sync(~0u, most);
-  if (lane == 31) s.warp[wid] = x, s.least[wid] = least, s.most[wid] = most;
-  __syncthreads();
-  long long before = 0, W = 0;
-  for (int i = 0; i < warps; ++i) {
-    if (i < wid) before += s.warp[i];
-    W += s.warp[i];
-    least = min(least, s.least[i]);
-    most = max(most, s.most[i]);
-  }
-  before += x - sum;
-  if (pre) {
-    int lo, hi;
-    pre_keys(a, least, most, lo, hi);
-    const int nt = tiles_of(lo, hi, ph.tile);
-    W = (long long)ph.items * nt;
-    const int n = ctas_of(ph.n, W);
-    if (cta >= n) return false;
-    long long c[2];
-    for (int k = 0; k < 2; ++k) {
-      const long long r = raw_cut(cta + k, W, n);
-      const long long it = r / nt;
-      c[k] = snap(r, it * nt, nt);
-    }
-    if (c[0] >= c[1]) return false;
-    end = c[1];
-    w.x = c[0];
-    w.item = (int)(c[0] / nt);
-    w.s = (long long)w.item * nt;
-    w.b = 0;
-    w.h = w.item / ph.rt;
-    w.r = w.item - w.h * ph.rt;
-    w.lo = lo;
-    w.hi = hi;
-    w.nt = nt;
-    w.len = 0;
-    return true;
-  }
-  const int n = ctas_of(ph.n, W);
-  if (cta >= n) return false;
-  // the thread whose sequences hold a cut places it
-  for (int k = 0; k < 2; ++k) {
-    const long long r = raw_cut(cta + k, W, n);
-    const bool last = r == W;
-    if (sum > 0 && r >= before && (r < before + sum || (last && before + sum == W))) {
-      long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        int lo, hi;
-        own_keys(a, len_of(a, b), lo, hi);
-        const int nt = tiles_of(lo, hi, ph.tile);
-        const long long all = (long long)nt * per_b;
-        if (r < at + all || (last && b == b1 - 1)) {
-          const long long it = last ? per_b - 1 : (r - at) / nt;
-          s.cut[k] = last ? W : snap(r, at + it * nt, nt);
-          s.cut_b[k] = b;
-          s.start[k] = at;
-          break;
-        }
-        at += all;
-      }
-    }
-  }
-  __syncthreads();
-  if (s.cut[0] >= s.cut[1]) return false;
-  end = s.cut[1];
-  w.x = s.cut[0];
-  w.b = s.cut_b[0];
-  long long at = s.start[0];
-  w.len = len_of(a, w.b);
-  own_keys(a, w.len, w.lo, w.hi);
-  w.nt = tiles_of(w.lo, w.hi, ph.tile);
-  if (w.x >= at + (long long)w.nt * per_b) {   // moved to the next sequence's first tile
-    at += (long long)w.nt * per_b;
-    ++w.b;
-    w.len = len_of(a, w.b);
-    own_keys(a, w.len, w.lo, w.hi);
-    w.nt = tiles_of(w.lo, w.hi, ph.tile);
-  }
-  const int in = (int)((w.x - at) / w.nt);
-  w.s = at + (long long)in * w.nt;
-  w.h = in / ph.rt;
-  w.r = in - w.h * ph.rt;
-  w.item = w.b * per_b + in;
-  return true;
-}
-
-// The next piece of the walk (w.x < end), which it moves past.
-__device__ __forceinline__ Piece next(const PagedArgs& a, const Phase& ph, bool pre, int cta,
-                                      long long end, Walk& w) {
+// The next piece of the walk (w.x < w.end), which it moves past.
+__device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, int i, Walk& w) {
+  const Phase& ph = pre ? a.pre : a.own;
   Piece p;
   p.h = w.h;
   p.b = w.b;
+  p.len = w.len;
+  p.table = w.slot;
   p.lo = w.lo;
   p.hi = w.hi;
-  const int all = pre ? a.B * a.TG : a.TG;
   p.row0 = w.r * ph.rows;
-  p.rows = min(ph.rows, all - p.row0);
-  if (!pre) p.row0 += w.b * a.TG;
-  const int from = (int)(w.x - w.s);
-  const int to = (int)min((long long)w.nt, end - w.s);
+  p.rows = min(ph.rows, (pre ? a.B * a.TG : a.TG) - p.row0);
+  const int from = w.x - w.s, to = min(w.u, w.end - w.s);
   const int base = w.lo / ph.tile;
-  p.t0 = base + from;
-  p.t1 = base + to;
-  const bool whole = from == 0 && to == w.nt;
-  p.slot = whole && a.shared == 0 ? -1 : (from == 0 ? w.item : ph.items + cta);
+  p.t0 = base + max(0, from - kOver);
+  p.t1 = base + to - kOver;
+  p.slot = from == 0 && to == w.u && a.shared == 0 ? -1 : (from == 0 ? w.item : ph.items + i);
   w.x = w.s + to;
-  if (w.x < end) {
+  if (w.x < w.end) {
     w.s = w.x;
     ++w.item;
     if (++w.r == ph.rt) {
       w.r = 0;
       if (++w.h == a.c.Hkv && !pre) {
         w.h = 0;
-        ++w.b;
-        w.len = len_of(a, w.b);
-        own_keys(a, w.len, w.lo, w.hi);
-        w.nt = tiles_of(w.lo, w.hi, ph.tile);
+        advance(a, w);
       }
     }
   }
   return p;
 }
 
-// Keys [lo, hi) that packed row r sees in the phase, and where it is in Q and O.
+// Keys [lo, hi) that a packed row sees in the phase, and its index in LSE (and,
+// times d, in Q and O).
 struct Row {
-  int lo, hi;
-  long long at;      // element offset of its d values
-  long long lse;     // offset in LSE
+  int lo, hi, out;
 };
-__device__ __forceinline__ Row row_of(const PagedArgs& a, bool pre, int h, int r) {
+__device__ __forceinline__ Row row_at(const PagedArgs& a, bool pre, int h, int b, int q, int len) {
   Row o;
-  const int b = r / a.TG, q = r - b * a.TG, t = q / a.G, g = q - t * a.G;
-  const int len = len_of(a, b);
-  const int pos = len - a.T + t;
+  const int pos = len - a.T + q % a.T;
   o.lo = pre ? 0 : a.shared;
   o.hi = a.causal ? max(0, min(len, pos + 1)) : len;
   if (pre) o.hi = min(o.hi, a.shared);
   if (a.wl >= 0) o.lo = max((long long)o.lo, (long long)pos - a.wl);
-  o.lse = ((long long)b * a.Hq + h * a.G + g) * a.T + t;
-  o.at = o.lse * a.c.d;
+  o.out = (b * a.Hq + h * a.G) * a.T + q;
   return o;
+}
+// Row r of a piece.
+__device__ __forceinline__ Row row_of(const PagedArgs& a, bool pre, const Piece& p, int r) {
+  if (!pre) return row_at(a, false, p.h, p.b, p.row0 + r, p.len);
+  const int b = (p.row0 + r) / a.TG;
+  return row_at(a, true, p.h, b, p.row0 + r - b * a.TG, len_of(a, b));
+}
+
+// The table row of a slot (slot 0's for one out of range, whose sequence has no keys).
+__device__ __forceinline__ const int* table_row(const PagedArgs& a, int slot) {
+  if ((unsigned)slot >= (unsigned)a.c.slots) slot = 0;
+  return a.c.table + (long long)slot * a.c.width;
 }
 
 // Byte offset of key j (head h) in the layer's K or V, through a table row.
 __device__ __forceinline__ long long key_offset(const CacheView& c, const int* trow, int h, int j) {
-  int page = trow[j >> c.page_log2];
+  int page = __ldg(trow + (j >> c.page_log2));
   if ((unsigned)page >= (unsigned)c.pages) page = 0;
   return page * c.page_stride + (long long)h * c.head_bytes +
          (long long)(j & ((1 << c.page_log2) - 1)) * c.row_bytes;
-}
-
-// The table row of a piece: the first sequence's in the shared phase.
-__device__ __forceinline__ const int* table_row(const PagedArgs& a, int b) {
-  int s = slot_of(a, b);
-  if ((unsigned)s >= (unsigned)a.c.slots) s = 0;
-  return a.c.table + (long long)s * a.c.width;
 }
 
 }  // namespace sched

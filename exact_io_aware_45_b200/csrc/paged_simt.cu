@@ -21,8 +21,8 @@
 namespace fa {
 namespace {
 
-constexpr int kRows = 8;
-constexpr int kTile = 32;
+constexpr int kRows = kSimtRows;
+constexpr int kTile = kSimtTile;
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -63,12 +63,11 @@ __device__ __forceinline__ void store_f(__nv_bfloat16* p, float x) { *p = __floa
 template <typename T, int D>
 struct SimtShared {
   alignas(16) float q[kRows][D];                      // read as float4
-  sched::Scratch scratch;
   float p[kWarps][kRows][kTile];
   float o[kWarps][kRows][D];
   float m[kWarps][kRows], l[kWarps][kRows];
   int lo[kRows], hi[kRows];
-  long long at[kRows], lse[kRows];
+  int out[kRows];
 };
 
 template <typename T, int D>
@@ -79,17 +78,16 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Phase& ph = pre ? a.pre : a.own;
   sched::Walk w;
-  long long end;
-  if (!sched::begin(a, ph, pre, blockIdx.x, kWarps * 32, s.scratch, w, end)) return;
+  if (!sched::begin(a, pre, blockIdx.x, w)) return;   // the block's warps walk alike
   const T* Q = static_cast<const T*>(a.Q);
-  while (w.x < end) {
-    const sched::Piece pc = sched::next(a, ph, pre, blockIdx.x, end, w);
+  while (w.x < w.end) {
+    const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
     __syncthreads();
     if (tid < kRows) {
       sched::Row r;
-      r.lo = r.hi = 0, r.at = r.lse = 0;
-      if (tid < pc.rows) r = sched::row_of(a, pre, pc.h, pc.row0 + tid);
-      s.lo[tid] = r.lo, s.hi[tid] = r.hi, s.at[tid] = r.at, s.lse[tid] = r.lse;
+      r.lo = r.hi = r.out = 0;
+      if (tid < pc.rows) r = sched::row_of(a, pre, pc, tid);
+      s.lo[tid] = r.lo, s.hi[tid] = r.hi, s.out[tid] = r.out;
     }
     __syncthreads();
     for (int i = tid; i < kRows * D; i += kWarps * 32) {
@@ -97,7 +95,7 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
       float x = 0.f;
       if (r < pc.rows) {
         float y[1];
-        load_f<1>(Q + s.at[r] + i % D, y);
+        load_f<1>(Q + (size_t)s.out[r] * D + i % D, y);
         x = y[0] * a.scale;
       }
       s.q[r][i % D] = x;
@@ -110,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
 #pragma unroll
       for (int i = 0; i < kPer; ++i) o[r][i] = 0.f;
     }
-    const int* trow = sched::table_row(a, pc.b);
+    const int* trow = sched::table_row(a, pc.table);
     for (int t = pc.t0 + warp; t < pc.t1; t += kWarps) {
       const int j = t * kTile + lane;
       const bool in = j >= pc.lo && j < pc.hi;
@@ -203,8 +201,8 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
       const float y = sum > 0.f ? acc / sum : (sum == 0.f ? 0.f : acc);
       const float lse2 = top + log2f(sum);
       if (pc.slot < 0) {
-        store_f(static_cast<T*>(a.O) + s.at[r] + e, y);
-        if (e == 0) a.LSE[s.lse[r]] = lse2 * 0.6931471805599453f;
+        store_f(static_cast<T*>(a.O) + (size_t)s.out[r] * D + e, y);
+        if (e == 0) a.LSE[s.out[r]] = lse2 * 0.6931471805599453f;
       } else {
         const long long at = (long long)pc.slot * ph.rows + r;
         ph.o[at * D + e] = y;
@@ -234,116 +232,104 @@ cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
 // ---------------------------------------------------------------- join
 
 // O = sum_p 2^(lse_p - lse) O_p, lse = log2 sum_p 2^lse_p over a row's partial
-// results. One block per sequence and KV head (and kJoinRows rows), one warp a
-// row. The pieces of an item follow from the same arithmetic that cut them. Reads
-// (d + 1) floats a piece and row, from L2 mostly.
-constexpr int kJoinWarps = 4;
-constexpr int kJoinRows = 16;
+// results, whose slots follow from the same arithmetic that cut them. A warp
+// has a row (kSplit = 1), or all warps of a block share one and meet in shared memory:
+// few rows have many pieces each (a long sequence is cut into hundreds), and one
+// warp would go through them for longer than the attention took. Reads (d + 1)
+// floats a piece and row, from L2 mostly.
+constexpr int kJoinWarps = 8;
 
-template <typename T, int D>
+template <typename T, int D, bool kShare>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
-  __shared__ long long part[kJoinWarps][2];
-  __shared__ int least_of[kJoinWarps], most_of[kJoinWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x - b * a.c.Hkv;
-  const int per_b = a.c.Hkv * a.own.rt;
-  long long before = 0, W = 0;
-  int least = 0x7fffffff, most = 0;
-  for (int i = tid; i < a.B; i += kJoinWarps * 32) {
-    const int len = sched::len_of(a, i);
+  __shared__ float part_o[kShare ? kJoinWarps : 1][D], part_lse[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = kShare ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
+  if (row >= a.B * a.c.Hkv * a.TG) return;
+  const int bh = row / a.TG, q = row - bh * a.TG;
+  const int b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
+  const sched::Batch t = sched::scan_batch(a, b);
+  const sched::Cuts cuts(t.W, a.own.n);
+  const int u = sched::own_units(a, sched::len_of(a, b));
+  const int r = q / a.own.rows, in = h * a.own.rt + r;
+  int first, more, pre_first = 0, pre_more = -1, pre_item = 0, pre_row = 0;
+  sched::pieces_of(t.before + in * u, u, cuts, first, more);
+  if (a.shared) {
     int lo, hi;
-    sched::own_keys(a, len, lo, hi);
-    const long long t = (long long)sched::tiles_of(lo, hi, a.own.tile) * per_b;
-    W += t;
-    if (i < b) before += t;
-    least = min(least, len);
-    most = max(most, len);
+    sched::pre_keys(a, t.least, t.most, lo, hi);
+    const int pu = sched::units_of(lo, hi, a.pre.tile), pr = b * a.TG + q;
+    pre_item = h * a.pre.rt + pr / a.pre.rows;
+    pre_row = pr % a.pre.rows;
+    sched::pieces_of(pre_item * pu, pu, sched::Cuts(a.pre.items * pu, a.pre.n), pre_first,
+                     pre_more);
+  } else if (more == 0) {
+    return;                                             // written by its only piece
   }
+  const int own_count = more + 1, count = own_count + pre_more + 1;
+  // row index of partial p in its phase's buffers
+  auto at_of = [&](int p) -> long long {
+    if (p < own_count)
+      return (long long)(p == 0 ? b * a.c.Hkv * a.own.rt + in : a.own.items + first + p) *
+                 a.own.rows + (q - r * a.own.rows);
+    p -= own_count;
+    return (long long)(p == 0 ? pre_item : a.pre.items + pre_first + p) * a.pre.rows + pre_row;
+  };
+  float top = -INFINITY;
+  for (int p = lane; p < count; p += 32)
+    top = fmaxf(top, (p < own_count ? a.own.lse : a.pre.lse)[at_of(p)]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(~0u, before, o);
-    W += __shfl_xor_sync(~0u, W, o);
-  }
-  least = __reduce_min_sync(~0u, least);
-  most = __reduce_max_sync(~0u, most);
-  if (lane == 0) {
-    part[warp][0] = before, part[warp][1] = W;
-    least_of[warp] = least, most_of[warp] = most;
-  }
-  __syncthreads();
-  before = W = 0;
-  for (int i = 0; i < kJoinWarps; ++i) {
-    before += part[i][0], W += part[i][1];
-    least = min(least, least_of[i]);
-    most = max(most, most_of[i]);
-  }
-  int lo, hi;
-  sched::own_keys(a, sched::len_of(a, b), lo, hi);
-  const int nt = sched::tiles_of(lo, hi, a.own.tile);
-  const int n = sched::ctas_of(a.own.n, W);
-  sched::pre_keys(a, least, most, lo, hi);
-  const int pre_nt = a.shared ? sched::tiles_of(lo, hi, a.pre.tile) : 0;
-  const long long pre_W = (long long)a.pre.items * pre_nt;
-  const int pre_n = a.shared ? sched::ctas_of(a.pre.n, pre_W) : 0;
-  const int q1 = min(a.TG, (int)(blockIdx.y + 1) * kJoinRows);
-  for (int q = blockIdx.y * kJoinRows + warp; q < q1; q += kJoinWarps) {
-    const int r = q / a.own.rows;
-    const int in = h * a.own.rt + r;
-    int first, more, pre_first = 0, pre_more = -1, pre_item = 0, pre_row = 0;
-    sched::pieces_of(before + (long long)in * nt, nt, W, n, first, more);
-    if (a.shared) {
-      const int pr = b * a.TG + q;
-      pre_item = h * a.pre.rt + pr / a.pre.rows;
-      pre_row = pr % a.pre.rows;
-      sched::pieces_of((long long)pre_item * pre_nt, pre_nt, pre_W, pre_n, pre_first, pre_more);
-    } else if (more == 0) {
-      continue;                                       // written by the only piece
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int p = kShare ? warp : 0; p < count; p += kShare ? kJoinWarps : 1) {
+    const long long at = at_of(p);
+    const float c = exp2f((p < own_count ? a.own.lse : a.pre.lse)[at] - ref);
+    sum += c;
+    if (lane * kPer < D) {
+      float v[kPer];
+      load_f<kPer>((p < own_count ? a.own.o : a.pre.o) + at * D + lane * kPer, v);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
     }
-    const int own_count = more + 1, count = own_count + pre_more + 1;
-    // row index of partial p in its phase's buffers
-    auto at_of = [&](int p) -> long long {
-      if (p < own_count)
-        return (long long)(p == 0 ? b * per_b + in : a.own.items + first + p) * a.own.rows +
-               (q - r * a.own.rows);
-      p -= own_count;
-      return (long long)(p == 0 ? pre_item : a.pre.items + pre_first + p) * a.pre.rows + pre_row;
-    };
-    float top = -INFINITY;
-    for (int p = lane; p < count; p += 32)
-      top = fmaxf(top, (p < own_count ? a.own.lse : a.pre.lse)[at_of(p)]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < count; ++p) {
-      const long long at = at_of(p);
-      const float c = exp2f((p < own_count ? a.own.lse : a.pre.lse)[at] - ref);
-      sum += c;
-      if (lane * kPer < D) {
-        float v[kPer];
-        load_f<kPer>((p < own_count ? a.own.o : a.pre.o) + at * D + lane * kPer, v);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
-      }
-    }
-    const sched::Row row = sched::row_of(a, false, h, b * a.TG + q);
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  }
+  if constexpr (kShare) {
     if (lane * kPer < D)
 #pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        store_f(static_cast<T*>(a.O) + row.at + lane * kPer + e, acc[e] * inv);
-    if (lane == 0) a.LSE[row.lse] = (top + log2f(sum)) * 0.6931471805599453f;
+      for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
+    if (lane == 0) part_lse[warp] = sum;
+    __syncthreads();
+    if (warp) return;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) {
+      sum += part_lse[k];
+      if (lane * kPer < D)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] += part_o[k][lane * kPer + e];
+    }
   }
+  const size_t out = (size_t)(b * a.Hq + h * a.G) * a.T + q;
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  if (lane * kPer < D)
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      store_f(static_cast<T*>(a.O) + out * D + lane * kPer + e, acc[e] * inv);
+  if (lane == 0) a.LSE[out] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, cudaStream_t st) {
-  const dim3 grid(a.B * a.c.Hkv, (a.TG + kJoinRows - 1) / kJoinRows);
-  join_kernel<T, D><<<grid, kJoinWarps * 32, 0, st>>>(a);
+  const int rows = a.B * a.c.Hkv * a.TG;
+  // with fewer rows than warps on the device, a block per row keeps it busier
+  if (rows <= 1184)
+    join_kernel<T, D, true><<<rows, kJoinWarps * 32, 0, st>>>(a);
+  else
+    join_kernel<T, D, false><<<(rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }

@@ -319,17 +319,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
-// 5-D tiled load of one box at {0, row, 0, head, page} (make_tmap_pages).
-__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* m, uint64_t* bar,
-                                              int row, int head, int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(head),
-      "r"(page)
-      : "memory");
-}
-
 // Plain (untiled) bulk copy global -> shared; addresses and size 16-byte multiples.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -601,12 +590,6 @@ bool make_tmap_3d_strided(CUtensorMap* m, const void* base, CUtensorMapDataType 
                           int elem_bytes, uint64_t cols, uint64_t rows, uint64_t planes,
                           uint64_t row_stride, uint64_t plane_stride, uint32_t box_cols,
                           uint32_t box_rows, CUtensorMapSwizzle swz);
-// Map of one layer of a paged bf16 cache, [pages][heads][page_size][d] with
-// `page_stride` bytes between pages and d in {64, 128}, seen as {64 columns, row,
-// column half, head, page}: one box is `box_rows` rows of one head of one page,
-// all d columns, in halves of 64 columns (128-byte swizzled rows).
-bool make_tmap_pages(CUtensorMap* m, const void* base, int d, int page_size, int heads, int pages,
-                     long long page_stride, int box_rows);
 // Sets cudaFuncAttributeMaxDynamicSharedMemorySize of kernel `fn` to `bytes`
 // on the current device, once per (device, kernel, size); thread-safe.
 cudaError_t set_max_dynamic_smem(const void* fn, int bytes);

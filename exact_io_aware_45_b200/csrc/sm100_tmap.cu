@@ -65,22 +65,6 @@ bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int 
   return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_pages(CUtensorMap* m, const void* base, int d, int page_size, int heads, int pages,
-                     long long page_stride, int box_rows) {
-  EncodeTiled fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t row = (cuuint64_t)d * 2;
-  cuuint64_t dims[5] = {64, (cuuint64_t)page_size, (cuuint64_t)d / 64, (cuuint64_t)heads,
-                        (cuuint64_t)pages};
-  cuuint64_t strides[4] = {row, 128, row * page_size, (cuuint64_t)page_stride};
-  cuuint32_t box[5] = {64, (cuuint32_t)box_rows, (cuuint32_t)d / 64, 1, 1};
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 cudaError_t set_max_dynamic_smem(const void* fn, int bytes) {
   // The attribute belongs to the device that is current when it is set, so
   // it is set once per (device, kernel, size); host threads share the record.
