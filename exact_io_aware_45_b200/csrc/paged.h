@@ -49,15 +49,13 @@ struct Phase {
   int rt = 0;          // row tiles per (sequence, KV head); per KV head in the shared phase
   int n = 0;           // streams
   int items = 0;
-  float* o = nullptr;  // partial results: [items + n][rows][d], normalised
-  float* lse = nullptr;  // [items + n][rows], base 2
+  int fold = 1;        // partial results per piece and row
+  int over = 4;        // units of an item beside its tiles
+  int snap = 4;        // tiles that a cut keeps from an item's ends
+  int least = 12;      // units that a stream is worth
+  float* o = nullptr;  // partial results: [items + n][fold][rows][d], normalised
+  float* lse = nullptr;  // [items + n][fold][rows], base 2
 };
-
-namespace sched {
-// Units of an item beside its tiles, tiles that a cut keeps from an item's ends,
-// and units that a stream is worth.
-constexpr int kOver = 4, kSnap = 4, kMinUnits = 12;
-}  // namespace sched
 
 struct PagedArgs {
   CacheView c;
@@ -82,6 +80,10 @@ constexpr int kSimtRows = 8, kSimtTile = 32, kSimtBlocksPerSm = 4;
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
 constexpr int kMmaMaxRows = 16, kMmaWarps = 8;
 constexpr int mma_tile(int d) { return d == 128 ? 16 : 32; }
+// tcgen05 kernel for many packed rows (bf16, d in {64, 128}); a stream is a CTA.
+// fold = 2: one query tile of 128 rows, its key tiles dealt to two warpgroups.
+cudaError_t paged_tc(const PagedArgs& a, bool pre, cudaStream_t st);
+constexpr int kTcTile = 128, kTcRows = 128;
 // Joins the partial results of both phases.
 cudaError_t paged_join(const PagedArgs& a, int dtype, cudaStream_t st);
 

@@ -81,26 +81,53 @@ int sm_count() {
   return n;
 }
 
+// Kernels of a phase: bf16 with d of 64 or 128 runs on the tensor cores, all else
+// on the CUDA cores. Up to kMmaMaxRows packed rows the mma.sync kernel reads K
+// and V at full bandwidth; above, it would read them once per kMmaMaxRows rows, and
+// the tcgen05 kernel takes 128 or 256 rows at once.
+enum Family { kSimt, kMma, kTc };
+Family family(const CacheView& v, int rows) {
+  if (v.row_bytes != 2 * v.d || v.d < 64) return kSimt;
+  return rows <= kMmaMaxRows ? kMma : kTc;
+}
+
 // The work division of a phase of `groups` sequences and KV heads with `rows`
 // packed rows each. It depends on sizes and types only, so the workspace query
-// and the call agree. bf16 with d of 64 or 128 runs on the tensor cores, all
-// else on the CUDA cores.
-bool on_mma(const CacheView& v) { return v.row_bytes == 2 * v.d && v.d >= 64; }
-
+// and the call agree.
 Phase divide(const CacheView& v, int groups, int rows, int sms) {
   Phase p;
-  if (on_mma(v)) {
-    p.rows = rows <= 8 ? 8 : kMmaMaxRows;
-    p.tile = mma_tile(v.d);
-    p.n = sms * kMmaWarps;
-  } else {
-    p.rows = kSimtRows;
-    p.tile = kSimtTile;
-    p.n = sms * kSimtBlocksPerSm;
+  switch (family(v, rows)) {
+    case kSimt:
+      p.rows = kSimtRows;
+      p.tile = kSimtTile;
+      p.n = sms * kSimtBlocksPerSm;
+      break;
+    case kMma:
+      p.rows = rows <= 8 ? 8 : kMmaMaxRows;
+      p.tile = mma_tile(v.d);
+      p.n = sms * kMmaWarps;
+      break;
+    case kTc:
+      p.fold = rows <= kTcRows ? 2 : 1;
+      p.rows = p.fold == 2 ? kTcRows : 2 * kTcRows;
+      p.tile = kTcTile;
+      p.n = sms;
+      p.over = 1;
+      p.snap = 1;
+      p.least = 3;
+      break;
   }
   p.rt = (rows + p.rows - 1) / p.rows;
   p.items = groups * p.rt;
   return p;
+}
+
+cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) {
+  switch (family(a.c, pre ? a.B * a.TG : a.TG)) {
+    case kSimt: return paged_simt(a, pre, dtype, st);
+    case kMma: return paged_mma(a, pre, st);
+    default: return paged_tc(a, pre, st);
+  }
 }
 
 // Fills in both phases; false if their units do not fit an int.
@@ -108,13 +135,13 @@ bool plan(PagedArgs& a, int sms) {
   a.own = divide(a.c, a.B * a.c.Hkv, a.TG, sms);
   a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, sms) : Phase();
   const long long keys = (long long)a.c.width << a.c.page_log2;
-  const long long most = keys / a.own.tile + 2 + sched::kOver;
+  const long long most = keys / 16 + 8;
   return a.own.items * most < (1ll << 31) - (1 << 20) &&
          a.pre.items * most < (1ll << 31) - (1 << 20);
 }
 
 size_t phase_bytes(const Phase& p, int d, size_t* lse_at) {
-  const size_t rows = (size_t)(p.items + p.n) * p.rows;
+  const size_t rows = (size_t)(p.items + p.n) * p.rows * p.fold;
   *lse_at = align256(rows * d * 4);
   return *lse_at + align256(rows * 4);
 }
@@ -176,11 +203,9 @@ fa_status fwd(const fa_cache* cache, int layer, const void* Q, void* O, float* L
   a.pre.o = reinterpret_cast<float*>(w + own);
   a.pre.lse = reinterpret_cast<float*>(w + own + pre_lse);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  for (int pre = shared ? 1 : 0; pre >= 0; --pre) {
-    const cudaError_t e =
-        on_mma(v) ? paged_mma(a, pre != 0, st) : paged_simt(a, pre != 0, cache->dtype, st);
-    if (e != cudaSuccess) return from_cuda(e);
-  }
+  if (shared)
+    if (cudaError_t e = run_phase(a, true, cache->dtype, st)) return from_cuda(e);
+  if (cudaError_t e = run_phase(a, false, cache->dtype, st)) return from_cuda(e);
   return from_cuda(paged_join(a, cache->dtype, st));
 }
 

@@ -2,14 +2,14 @@
 // compute partial results and the kernel that joins them.
 //
 // A phase's items (row tiles of packed query rows over one key range) are laid
-// end to end as W units: kOver for an item's set-up and result, then one for each
+// end to end as W units: Phase::over for an item's set-up and result, then one for each
 // key tile. Stream i of n (a warp, or a block) takes units [x_i, x_{i+1}), all
 // streams as even as whole units allow: the load does not depend on how the
 // lengths are spread, and no length has to be known on the host. A cut in an item's first
-// kOver units or closer than kSnap tiles to either end moves to that end, which
-// spares partial results of a few tiles; n shrinks to W / kMinUnits for little work.
+// `over` units or closer than `snap` tiles to either end moves to that end, which
+// spares partial results of a few tiles; n shrinks to W / `least` for little work.
 //
-// An item that one stream covers whole and that no other phase adds to is written
+// An item that one stream covers whole and that nothing else adds to is written
 // to O and LSE directly. Otherwise each of its pieces goes to a slot of its
 // own: the piece with the item's first tile to slot `item`, a piece that begins
 // with stream i's first tile to slot items + i.
@@ -44,13 +44,13 @@ __device__ __forceinline__ void own_keys(const PagedArgs& a, int len, int& lo, i
   // the window bound of the first query; in 64 bits, wl may be any int
   if (a.wl >= 0) lo = max((long long)lo, (long long)len - a.T - a.wl);
 }
-__device__ __forceinline__ int units_of(int lo, int hi, int tile) {
-  return kOver + (hi > lo ? (hi - 1) / tile - lo / tile + 1 : 1);
+__device__ __forceinline__ int units_of(const Phase& ph, int lo, int hi) {
+  return ph.over + (hi > lo ? (hi - 1) / ph.tile - lo / ph.tile + 1 : 1);
 }
 __device__ __forceinline__ int own_units(const PagedArgs& a, int len) {
   int lo, hi;
   own_keys(a, len, lo, hi);
-  return units_of(lo, hi, a.own.tile);
+  return units_of(a.own, lo, hi);
 }
 
 // Keys [lo, hi) that any query sees of the shared prefix, from the smallest and
@@ -65,8 +65,8 @@ __device__ __forceinline__ void pre_keys(const PagedArgs& a, int least, int most
 // W units in n even ranges: the first `extra` are one longer.
 struct Cuts {
   int W, n, each, extra;
-  __device__ Cuts(int units, int streams) : W(units) {
-    n = max(1, min(streams, W / kMinUnits));
+  __device__ Cuts(const Phase& ph, int units) : W(units) {
+    n = max(1, min(ph.n, W / ph.least));
     each = W / n;
     extra = W - each * n;
   }
@@ -83,15 +83,16 @@ struct Cuts {
 };
 
 // The cut x, moved to an end of its item [s, s + u) when it lies close to one.
-__device__ __forceinline__ int snap(int x, int s, int u) {
-  if (x - s < kOver + kSnap) return s;
-  if (s + u - x < kSnap) return s + u;
+__device__ __forceinline__ int snap(const Phase& ph, int x, int s, int u) {
+  if (x - s < ph.over + ph.snap) return s;
+  if (s + u - x < ph.snap) return s + u;
   return x;
 }
 
 // Pieces of the item [s, s + u): streams first + 1 .. first + more begin inside it.
-__device__ __forceinline__ void pieces_of(int s, int u, const Cuts& c, int& first, int& more) {
-  const int a = s + kOver + kSnap, b = s + u - kSnap;   // cuts in [a, b] stay inside
+__device__ __forceinline__ void pieces_of(const Phase& ph, int s, int u, const Cuts& c, int& first,
+                                          int& more) {
+  const int a = s + ph.over + ph.snap, b = s + u - ph.snap;   // cuts in [a, b] stay inside
   first = more = 0;
   if (b < a) return;
   first = c.first(a) - 1;
@@ -144,7 +145,7 @@ __device__ __forceinline__ void enter(const PagedArgs& a, int b, Walk& w) {
   w.len = len_at(a, w.slot);
   w.len1 = len_at(a, w.slot1);
   own_keys(a, w.len, w.lo, w.hi);
-  w.u = units_of(w.lo, w.hi, a.own.tile);
+  w.u = units_of(a.own, w.lo, w.hi);
 }
 __device__ __forceinline__ void advance(const PagedArgs& a, Walk& w) {
   ++w.b;
@@ -154,7 +155,7 @@ __device__ __forceinline__ void advance(const PagedArgs& a, Walk& w) {
   w.len1 = len_at(a, w.slot1);
   w.slot2 = slot_ahead(a, w.b + 2);
   own_keys(a, w.len, w.lo, w.hi);
-  w.u = units_of(w.lo, w.hi, a.own.tile);
+  w.u = units_of(a.own, w.lo, w.hi);
 }
 
 // Sets up the walk of stream `i`; all lanes of a warp call it and get the same.
@@ -164,13 +165,13 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
   const Batch t = scan_batch(a, 0);
   if (pre) {
     pre_keys(a, t.least, t.most, w.lo, w.hi);
-    w.u = units_of(w.lo, w.hi, a.pre.tile);
-    const Cuts c(a.pre.items * w.u, a.pre.n);
+    w.u = units_of(a.pre, w.lo, w.hi);
+    const Cuts c(a.pre, a.pre.items * w.u);
     if (i >= c.n) return false;
     const int x0 = c.at(i), x1 = c.at(i + 1);
     w.item = x0 / w.u;
-    w.x = snap(x0, w.item * w.u, w.u);
-    w.end = x1 == c.W ? c.W : snap(x1, x1 / w.u * w.u, w.u);
+    w.x = snap(a.pre, x0, w.item * w.u, w.u);
+    w.end = x1 == c.W ? c.W : snap(a.pre, x1, x1 / w.u * w.u, w.u);
     if (w.x >= w.end) return false;
     if (w.x >= (w.item + 1) * w.u) ++w.item;
     w.s = w.item * w.u;
@@ -180,7 +181,7 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
     w.slot = slot_of(a, 0);
     return true;
   }
-  const Cuts c(t.W, a.own.n);
+  const Cuts c(a.own, t.W);
   if (i >= c.n) return false;
   const int per_b = a.c.Hkv * a.own.rt;
   const int x0 = c.at(i), x1 = c.at(i + 1);
@@ -203,12 +204,12 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
       b0 = g + k;
       at0 = __shfl_sync(~0u, from, k);
       const int v = __shfl_sync(~0u, u, k);
-      w.x = snap(x0, at0 + (x0 - at0) / v * v, v);
+      w.x = snap(a.own, x0, at0 + (x0 - at0) / v * v, v);
     }
     if (has1) {
       const int k = __ffs(has1) - 1;
       const int f = __shfl_sync(~0u, from, k), v = __shfl_sync(~0u, u, k);
-      w.end = snap(x1, f + (x1 - f) / v * v, v);
+      w.end = snap(a.own, x1, f + (x1 - f) / v * v, v);
     }
     base = __shfl_sync(~0u, to, 31);
   }
@@ -251,9 +252,10 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, int i, Walk&
   p.rows = min(ph.rows, (pre ? a.B * a.TG : a.TG) - p.row0);
   const int from = w.x - w.s, to = min(w.u, w.end - w.s);
   const int base = w.lo / ph.tile;
-  p.t0 = base + max(0, from - kOver);
-  p.t1 = base + to - kOver;
-  p.slot = from == 0 && to == w.u && a.shared == 0 ? -1 : (from == 0 ? w.item : ph.items + i);
+  p.t0 = base + max(0, from - ph.over);
+  p.t1 = base + to - ph.over;
+  const bool alone = from == 0 && to == w.u && a.shared == 0 && ph.fold == 1;
+  p.slot = alone ? -1 : (from == 0 ? w.item : ph.items + i);
   w.x = w.s + to;
   if (w.x < w.end) {
     w.s = w.x;

@@ -249,30 +249,34 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
   const int bh = row / a.TG, q = row - bh * a.TG;
   const int b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
   const sched::Batch t = sched::scan_batch(a, b);
-  const sched::Cuts cuts(t.W, a.own.n);
+  const sched::Cuts cuts(a.own, t.W);
   const int u = sched::own_units(a, sched::len_of(a, b));
   const int r = q / a.own.rows, in = h * a.own.rt + r;
   int first, more, pre_first = 0, pre_more = -1, pre_item = 0, pre_row = 0;
-  sched::pieces_of(t.before + in * u, u, cuts, first, more);
+  sched::pieces_of(a.own, t.before + in * u, u, cuts, first, more);
   if (a.shared) {
     int lo, hi;
     sched::pre_keys(a, t.least, t.most, lo, hi);
-    const int pu = sched::units_of(lo, hi, a.pre.tile), pr = b * a.TG + q;
+    const int pu = sched::units_of(a.pre, lo, hi), pr = b * a.TG + q;
     pre_item = h * a.pre.rt + pr / a.pre.rows;
     pre_row = pr % a.pre.rows;
-    sched::pieces_of(pre_item * pu, pu, sched::Cuts(a.pre.items * pu, a.pre.n), pre_first,
+    sched::pieces_of(a.pre, pre_item * pu, pu, sched::Cuts(a.pre, a.pre.items * pu), pre_first,
                      pre_more);
-  } else if (more == 0) {
+  } else if (more == 0 && a.own.fold == 1) {
     return;                                             // written by its only piece
   }
-  const int own_count = more + 1, count = own_count + pre_more + 1;
+  const int own_count = (more + 1) * a.own.fold;
+  const int count = own_count + (pre_more + 1) * a.pre.fold;
   // row index of partial p in its phase's buffers
   auto at_of = [&](int p) -> long long {
-    if (p < own_count)
-      return (long long)(p == 0 ? b * a.c.Hkv * a.own.rt + in : a.own.items + first + p) *
-                 a.own.rows + (q - r * a.own.rows);
-    p -= own_count;
-    return (long long)(p == 0 ? pre_item : a.pre.items + pre_first + p) * a.pre.rows + pre_row;
+    const bool own = p < own_count;
+    const Phase& ph = own ? a.own : a.pre;
+    if (!own) p -= own_count;
+    int f = 0;
+    if (ph.fold == 2) f = p & 1, p >>= 1;
+    const int slot = own ? (p == 0 ? b * a.c.Hkv * a.own.rt + in : a.own.items + first + p)
+                         : (p == 0 ? pre_item : a.pre.items + pre_first + p);
+    return ((long long)slot * ph.fold + f) * ph.rows + (own ? q - r * a.own.rows : pre_row);
   };
   float top = -INFINITY;
   for (int p = lane; p < count; p += 32)

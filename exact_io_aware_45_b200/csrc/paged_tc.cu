@@ -1,0 +1,526 @@
+// Paged attention for many query rows per KV head (a batch behind a shared
+// prefix, long chunks of new tokens): bound by the tensor cores and the softmax
+// between the two products, so S = Q K^T and O += P V run on tcgen05 with
+// S, P and O in tensor memory.
+//
+// A stream is a CTA (one per SM): it walks its share of the 128-key tiles
+// (paged_sched.cuh). Two softmax warpgroups keep the tensor core busy in
+// turn, in one of two forms:
+//  * two query tiles (more than 128 packed rows): warpgroup t has rows
+//    128 t .. 128 t + 127 of the item, and every K/V tile serves both;
+//  * one query tile: the warpgroups take the item's key tiles alternately, with running
+//    statistics and an accumulator each, and leave two partial results to the join.
+//
+// K and V pages are copied by three loader warps with cp.async (any page size;
+// a TMA box ends with its page, and at 16 tokens a page the boxes of one 128-key tile cost
+// their issuing thread 6,900 cycles, twice what the tile's products and softmax take).
+// They are written in the 128-byte swizzled layout of the MMA descriptors: 64-column
+// block cb at 16 KB * cb, row r at 128 r, 16-byte chunk c at c ^ (r & 7). A
+// tile is handed over once its copies have landed and a proxy fence has
+// made them visible to the tensor core.
+//
+// The running maximum is a reference that moves only when a tile exceeds it by 2^8 (the
+// recurrence holds for any reference), so most tiles leave the accumulator alone.
+// P is rounded to bf16 for the second product (the row sum takes it unrounded);
+// sums, statistics and O stay in fp32.
+#include <math.h>
+
+#include "paged_sched.cuh"
+#include "sm100_common.cuh"
+
+namespace fa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kLoaders = 3;            // warps 0, 2 and 3
+constexpr int kM = 128, kN = kTcTile;  // query rows and keys of a tile
+constexpr float kTau = 8.0f;           // slack of the reference maximum, log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxSlots = 8;
+
+// kTwo: two query tiles.
+template <int D, bool kTwo>
+struct Cfg {
+  static constexpr int kSlots = D == 64 ? 8 : (kTwo ? 4 : 5);
+  static constexpr int kTileBytes = kN * D * 2;      // one K or V tile
+  static constexpr int kQBytes = kM * D * 2;
+  static constexpr int kBlock = 128 * 128;           // one 64-column block
+  static constexpr int kStage = 128 * 128;           // 32 fp32 columns of 128 rows
+  static constexpr int kOffKV = (kTwo ? 2 : 1) * kQBytes;
+  static constexpr int kOffStage = kOffKV + kSlots * kTileBytes;
+  static constexpr int kBytes = kOffStage + 2 * kStage + 1024;
+  static constexpr uint32_t kS = 128;                // TMEM columns: S_t at 128 t,
+  static constexpr uint32_t kO = 256;                // O_t at 256 + D t,
+  static constexpr uint32_t kP = 64;                 // P_t in the upper half of S_t
+};
+
+struct Control {
+  uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_ready[2];
+  uint64_t done, never;
+  uint32_t tmem;
+  int abort, skip;
+};
+
+// Position of a tile in the order of loading and use, from the piece's first: two
+// query tiles use K0 V0 K1 V1 ..., one query tile K0 K1 V0 K2 V1 ... (the scores of
+// both warpgroups run ahead).
+template <bool kTwo>
+__device__ __forceinline__ uint32_t k_at(uint32_t j) {
+  return kTwo ? 2 * j : (j ? 2 * j - 1 : 0);
+}
+template <bool kTwo>
+__device__ __forceinline__ uint32_t v_at(uint32_t j, uint32_t tiles) {
+  return kTwo ? 2 * j + 1 : (j + 1 < tiles ? 2 * j + 2 : 2 * tiles - 1);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D, bool kTwo>
+__global__ void __launch_bounds__(kThreads, 1)
+    tc_kernel(const PagedArgs a, const bool pre, const long long stall) {
+  using C = Cfg<D, kTwo>;
+  constexpr uint32_t kSlots = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Control s;
+  uint8_t* const base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Phase& ph = pre ? a.pre : a.own;
+  sched::Walk w;
+  if (!sched::begin(a, pre, blockIdx.x, w)) return;      // the same answer in every warp
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(&s.kv_full[i], kLoaders);
+      mbar_init(&s.kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s.q_full[t], kTwo ? 4 : 8);
+      mbar_init(&s.s_full[t], 1);
+      mbar_init(&s.p_half[t], 4);
+      mbar_init(&s.p_full[t], 4);
+      mbar_init(&s.o_ready[t], 1);
+    }
+    mbar_init(&s.done, 1);
+    mbar_init(&s.never, 1);
+    s.abort = 0;
+    s.skip = *reinterpret_cast<volatile unsigned*>(a.c.err) & kErrTimeout;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = s.tmem;
+  if (s.skip) {                                          // nothing is in flight yet
+    __syncthreads();
+    if (warp == 2) tmem_dealloc(tm, 512);
+    return;
+  }
+  const Guard guard{&s.abort, a.c.err};
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_ready_first(bar, parity, guard);
+  };
+
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ loaders
+    const int me = warp == 0 ? 0 : warp - 1;
+    uint32_t n = 0, told = 0;                            // tiles issued, and handed over
+    // hands over the tiles below `to`, whose copies this warp has waited for
+    auto tell = [&](uint32_t to) {
+      if (to <= told) return;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (uint32_t i = told; i < to; ++i) mbar_arrive(&s.kv_full[i % kSlots]);
+      told = to;
+    };
+    bool ok = true;
+    while (ok && w.x < w.end) {
+      const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+      const int* trow = sched::table_row(a, pc.table);
+      const uint32_t tiles = pc.t1 - pc.t0;
+      const long long head = (long long)pc.h * a.c.head_bytes;
+      const int last = pc.hi > pc.lo ? (pc.hi - 1) >> a.c.page_log2 : -1;
+      for (uint32_t i = 0; i < 2 * tiles; ++i, ++n) {
+        // the i-th tile in order of use: which of K and V, and its index
+        uint32_t j;
+        bool is_v;
+        if (kTwo) {
+          j = i >> 1, is_v = i & 1;
+        } else {
+          is_v = i + 1 == 2 * tiles || (i && !(i & 1));
+          j = is_v ? (i + 1 == 2 * tiles ? tiles - 1 : i / 2 - 1) : (i + 1) / 2;
+        }
+        const uint32_t slot = n % kSlots;
+        if (n >= kSlots) {
+          uint64_t* bar = &s.kv_empty[slot];
+          const uint32_t parity = ((n / kSlots) & 1) ^ 1;
+          // before blocking, everything loaded is handed over: the tensor core may need it
+          // to get to the tile that frees this slot
+          if (!__all_sync(~0u, mbar_try_wait(bar, parity))) {
+            copy_wait<0>();
+            tell(n);
+            if (!__all_sync(~0u, wait(bar, parity))) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        const uint32_t to = smem_u32(base + C::kOffKV + slot * C::kTileBytes);
+        const int j0 = (pc.t0 + (int)j) * kN;
+        const char* from = is_v ? a.V : a.K;
+        // lane i knows the page of keys j0 + 16 i .. (pages hold 16 keys or more)
+        int page = 0;
+        {
+          const int e = (j0 + (lane & 7) * 16) >> a.c.page_log2;
+          if (e <= last) page = __ldg(trow + e);
+          if ((unsigned)page >= (unsigned)a.c.pages) page = 0;
+        }
+        const bool edge = j0 < pc.lo || j0 + kN > pc.hi;
+        constexpr int kVecs = D / 8, kRows = 32 / kVecs;  // chunks of a row; rows of an instruction
+        const int c = lane % kVecs;
+#pragma unroll 4
+        for (int r0 = me * kRows; r0 < kN; r0 += kLoaders * kRows) {
+          const int r = r0 + lane / kVecs;
+          const int pg = __shfl_sync(~0u, page, r0 >> 4);
+          const char* src = from + pg * a.c.page_stride + head +
+                            (long long)((j0 + r) & ((1 << a.c.page_log2) - 1)) * (D * 2) + c * 16;
+          // rows that no query sees are not read and count as zero
+          const int bytes = edge && (j0 + r < pc.lo || j0 + r >= pc.hi) ? 0 : 16;
+          copy16(to + (c >> 3) * C::kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, bytes);
+        }
+        copy_commit();
+        if (n >= 2) {
+          copy_wait<2>();
+          tell(n - 1);
+        }
+      }
+    }
+    copy_wait<0>();
+    if (ok) tell(n);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(kM, kN, false, false);
+      constexpr uint32_t id_o = idesc_bf16(kM, D, false, true);
+      const uint64_t dq0 = sdesc_sw128(smem_u32(base), 16, 1024);
+      const uint64_t dk0 = sdesc_sw128(smem_u32(base + C::kOffKV), 16, 1024);
+      const uint64_t dv0 = sdesc_sw128(smem_u32(base + C::kOffKV), C::kBlock, 1024);
+      auto slot_of = [&](uint32_t n) { return n % kSlots; };
+      auto have = [&](uint32_t n) { return wait(&s.kv_full[slot_of(n)], (n / kSlots) & 1); };
+      auto release = [&](uint32_t n) { mma_commit(&s.kv_empty[slot_of(n)]); };
+      // S_t = Q K^T with the tile at ring position n
+      auto issue_s = [&](int t, uint32_t n) {
+        const uint64_t dq = sdesc_at(dq0, kTwo ? t * C::kQBytes : 0);
+        const uint64_t dk = sdesc_at(dk0, slot_of(n) * C::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * C::kBlock + (k & 3) * 32;
+          mma_ss(tm + t * C::kS, sdesc_at(dq, off), sdesc_at(dk, off), id_s, k > 0);
+        }
+        mma_commit(&s.s_full[t]);
+      };
+      // O_t (+)= P_t V over keys 64 half .. 64 half + 63 of the tile at ring position n
+      auto issue_pv = [&](int t, uint32_t n, bool acc, int half) {
+        const uint64_t dv = sdesc_at(dv0, slot_of(n) * C::kTileBytes);
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int k = 4 * half + k4;
+          mma_ts(tm + C::kO + t * D, tm + t * C::kS + C::kP + k * 8, sdesc_at(dv, k * 16 * 128),
+                 id_o, acc || k > 0);
+        }
+      };
+      uint32_t cnt[2] = {0, 0};                          // tiles of each warpgroup so far
+      auto pv = [&](int t, uint32_t n, bool acc) {
+        if (!wait(&s.p_half[t], cnt[t] & 1)) return false;
+        tc_fence_after();
+        issue_pv(t, n, acc, 0);
+        if (!wait(&s.p_full[t], cnt[t] & 1)) return false;
+        tc_fence_after();
+        issue_pv(t, n, acc, 1);
+        ++cnt[t];
+        return true;
+      };
+      bool ok = injected_stall(&s.never, stall, guard);
+      uint32_t n0 = 0;
+      for (uint32_t np = 0; ok && w.x < w.end; ++np) {
+        const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+        const uint32_t tiles = pc.t1 - pc.t0;
+        if (kTwo) {
+          // the K tile serves both query tiles; warpgroup 1 runs half a tile behind
+          ok = wait(&s.q_full[0], np & 1) && have(n0);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, n0);
+          if (!(ok = wait(&s.q_full[1], np & 1))) break;
+          tc_fence_after();
+          issue_s(1, n0);
+          release(n0);
+          for (uint32_t j = 0; j < tiles; ++j) {
+            const bool more = j + 1 < tiles;
+            const uint32_t nv = n0 + v_at<true>(j, tiles), nk = n0 + k_at<true>(j + 1);
+            if (!(ok = have(nv) && (!more || have(nk)) && pv(0, nv, j > 0))) break;
+            if (more) issue_s(0, nk);
+            else mma_commit(&s.o_ready[0]);
+            if (!(ok = pv(1, nv, j > 0))) break;
+            release(nv);
+            if (more) {
+              issue_s(1, nk);
+              release(nk);
+            } else {
+              mma_commit(&s.o_ready[1]);
+            }
+          }
+        } else {
+          if (!(ok = wait(&s.q_full[0], np & 1))) break;
+          for (uint32_t j = 0; j < min(2u, tiles); ++j) {
+            const uint32_t nk = n0 + k_at<false>(j);
+            if (!(ok = have(nk))) break;
+            tc_fence_after();
+            issue_s(j, nk);
+            release(nk);
+          }
+          for (uint32_t j = 0; ok && j < tiles; ++j) {
+            const int t = j & 1;
+            const uint32_t nv = n0 + v_at<false>(j, tiles), nk = n0 + k_at<false>(j + 2);
+            const bool more = j + 2 < tiles;
+            if (!(ok = have(nv) && (!more || have(nk)) && pv(t, nv, j > 1))) break;
+            release(nv);
+            if (more) {
+              issue_s(t, nk);
+              release(nk);
+            }
+          }
+          if (ok) {
+            mma_commit(&s.o_ready[0]);
+            mma_commit(&s.o_ready[1]);
+          }
+        }
+        n0 += 2 * tiles;
+      }
+      // no MMA may still run when TMEM is freed, after an abort either
+      mma_commit(&s.done);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&s.done, 0) && clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;                       // warpgroup
+    const int r = (warp & 3) * 32 + lane;                // row of its query tile, TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_reg = tm + t * C::kS + lanes;
+    const uint32_t o_reg = tm + C::kO + t * D + lanes;
+    const bool xform = a.softcap > 0.f || a.scale <= 0.f;
+    const float scale2 = a.scale * kLog2e;
+    const float c = xform ? 1.f : scale2;
+    const float cap2 = a.softcap * kLog2e;
+    const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+    uint8_t* const stage = base + C::kOffStage + t * C::kStage;
+    const int tid = threadIdx.x - 128 - t * 128;
+    uint32_t cnt = 0;                                    // this warpgroup's tiles so far
+    for (uint32_t np = 0; w.x < w.end; ++np) {
+      const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+      const int ri = kTwo ? t * kM + r : r;              // row of the item
+      sched::Row row;
+      row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
+      if (ri < pc.rows) row = sched::row_of(a, pre, pc, ri);
+      {
+        // Q into its swizzled tile: this thread's row, or half of it
+        constexpr int kVecs = D / 8, kMine = kTwo ? kVecs : kVecs / 2;
+        const int4* from = reinterpret_cast<const int4*>(
+            static_cast<const __nv_bfloat16*>(a.Q) + (size_t)row.out * D);
+        uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + r * 128;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int v = kTwo ? i : t * kMine + i;
+          const int4 x = ri < pc.rows ? __ldg(from + v) : make_int4(0, 0, 0, 0);
+          *reinterpret_cast<int4*>(to + (v >> 3) * C::kBlock + (((v & 7) ^ (r & 7)) << 4)) = x;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_full[kTwo ? t : 0]);
+      }
+      const int lo_all = __reduce_max_sync(~0u, row.lo), hi_all = __reduce_min_sync(~0u, row.hi);
+      float m_ref = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = pc.t0 + (kTwo ? 0 : t); j < pc.t1; j += kTwo ? 1 : 2) {
+        if (!__all_sync(~0u, wait(&s.s_full[t], cnt & 1))) break;   // whole warps go on or not
+        tc_fence_after();
+        uint32_t x[128];
+        tmem_ld128(s_reg, x);
+        if (xform) {
+          if (a.softcap > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              x[i] = __float_as_uint(cap2 * tanh_ex2(__uint_as_float(x[i]) * to_cap));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * scale2);
+          }
+        }
+        const int j0 = j * kN;
+        if (j0 < lo_all || j0 + kN > hi_all) {
+          const int lo = row.lo - j0, hi = row.hi - j0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i < lo || i >= hi) x[i] = __float_as_uint(-INFINITY);
+        }
+        // row maximum in eight chains
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t* v = &x[16 * k];
+          float m = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+#pragma unroll
+          for (int i = 3; i < 15; i += 2)
+            m = fmax3(m, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          m8[k] = fmaxf(m, __uint_as_float(v[15]));
+        }
+        const float top = c * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                    fmaxf(m8[6], m8[7]));
+        const bool grow = top > m_ref + kTau;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2(m_ref - top);                      // 0 without a reference yet
+          m_ref = top;
+          l *= alpha;
+        }
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        const float2 c2 = make_float2(c, c), nmu2 = make_float2(-mu, -mu);
+        float2 acc[4] = {};
+        // P in two halves: P V of the first 64 keys starts while the second is computed
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 z = ffma2(make_float2(__uint_as_float(x[64 * hf + 2 * i]),
+                                               __uint_as_float(x[64 * hf + 2 * i + 1])), c2, nmu2);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+            acc[i & 3] = fadd2(acc[i & 3], e);
+            pk[i] = pack_bf16(e.x, e.y);
+          }
+          tmem_st32(s_reg + C::kP + 32 * hf, pk);
+          // earlier P V are complete (the commit behind S_t came after them)
+          if (hf == 0 && __any_sync(~0u, grow && !first)) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t o[32];
+              tmem_ld32(o_reg + k * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_reg + k * 32, o);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(hf ? &s.p_full[t] : &s.p_half[t]);
+        }
+        const float2 s01 = fadd2(acc[0], acc[1]), s23 = fadd2(acc[2], acc[3]);
+        l += (s01.x + s01.y) + (s23.x + s23.y);
+        first = false;
+        ++cnt;
+      }
+      // every S and P V of the piece has completed: its accumulators may be read,
+      // its Q buffers overwritten
+      bool got = wait(&s.o_ready[t], np & 1);
+      if (!kTwo) got = wait(&s.o_ready[t ^ 1], np & 1) && got;
+      const bool some = __all_sync(~0u, got) && !first;
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const float lse2 = m_ref + log2f(l);
+      const long long at = (long long)pc.slot * (ph.rows * ph.fold) + t * kM;   // partial row 0
+      if (ri < pc.rows) {
+        if (pc.slot < 0) a.LSE[row.out] = lse2 * kLn2;
+        else ph.lse[at + r] = lse2;
+      }
+      // rows through shared memory, 32 columns at a time, so that a warp writes lines
+      const int rows = min(kM, kTwo ? pc.rows - t * kM : pc.rows);
+      // of the tile's row 0 (own phase: the rows of a sequence and KV head are contiguous)
+      const int out0 = (pc.b * a.Hq + pc.h * a.G) * a.T + pc.row0 + t * kM;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        if (some) {
+          tmem_ld32(o_reg + k * 32, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(stage + r * 128 + ((q ^ (r & 7)) << 4)) =
+              make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                          __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        named_sync(1 + t, 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 16 + (tid >> 3), q = tid & 7;
+          const float4 v =
+              *reinterpret_cast<const float4*>(stage + rr * 128 + ((q ^ (rr & 7)) << 4));
+          if (rr < rows) {
+            if (pc.slot < 0) {
+              __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.O) +
+                                  (size_t)(out0 + rr) * D + k * 32 + q * 4;
+              *reinterpret_cast<uint2*>(to) =
+                  make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            } else {
+              *reinterpret_cast<float4*>(ph.o + (at + rr) * D + k * 32 + q * 4) = v;
+            }
+          }
+        }
+        named_sync(1 + t, 128);
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+template <int D, bool kTwo>
+cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
+  using C = Cfg<D, kTwo>;
+  static_assert(C::kBytes + sizeof(Control) <= 227 * 1024, "shared memory");
+  if (cudaError_t e =
+          set_max_dynamic_smem(reinterpret_cast<const void*>(tc_kernel<D, kTwo>), C::kBytes))
+    return e;
+  tc_kernel<D, kTwo><<<(pre ? a.pre : a.own).n, kThreads, C::kBytes, st>>>(
+      a, pre, debug_stall_cycles(kStallFwd));
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t paged_tc(const PagedArgs& a, bool pre, cudaStream_t st) {
+  const bool two = (pre ? a.pre : a.own).fold == 1;
+  if (a.c.d == 128) return two ? launch<128, true>(a, pre, st) : launch<128, false>(a, pre, st);
+  return two ? launch<64, true>(a, pre, st) : launch<64, false>(a, pre, st);
+}
+
+}  // namespace fa

@@ -351,7 +351,8 @@ fa_status fa_exp2_fma(const float* x, float* y, long long n, void* stream);
  * that start after the word is set do nothing. The call's outputs are then
  * undefined; nothing traps, faults or hangs, and after fa_get_device_error
  * has cleared the word the workspace works normally again.
- *   kernels: 0 (off) or an OR of FA_STALL_FWD (fa_fwd tensor-core kernel),
+ *   kernels: 0 (off) or an OR of FA_STALL_FWD (fa_fwd tensor-core kernel, and
+ *            the tcgen05 kernel of fa_fwd_paged and fa_fwd_shared),
  *            FA_STALL_BWD (backward main kernel), FA_STALL_DQ (the dQ kernel
  *            of fa_bwd_deterministic);
  *   wait_cycles: 1,000 .. 2,000,000,000 when kernels != 0 (ignored when 0).

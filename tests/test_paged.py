@@ -743,3 +743,38 @@ def test_paged_large_offsets():
     assert cache.table[1].tolist() == [2, 0, 1, -1]     # 3, pages - 7 and pages - 1, in order
     o2, lse2 = fa.forward_paged(q, cache, 0, ints([1]))
     check(o2, lse2, q, [x], [n], 0, "bf16", 1 / math.sqrt(128))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shared,B,T", [(0, 3, 9), (0, 2, 70), (64, 12, 1), (64, 90, 2)])
+def test_a_wait_that_runs_out_is_reported(d, shared, B, T):
+    """The injected wait ends the call without a fault; err says so, and later calls work."""
+    import time
+
+    import torch
+    lens = [400 + b for b in range(B)]
+    cache, seqs, dense = build(lens, 2, d, 16, "bf16", shared=shared)
+    q = torch.randn(B, 8, T, d, device="cuda").bfloat16()
+
+    def call():
+        return (fa.forward_shared(q, cache, 0, shared, seqs) if shared else
+                fa.forward_paged(q, cache, 0, seqs))
+
+    call()
+    torch.cuda.synchronize()
+    assert fa.fa_debug_set_stall(fa.FA_STALL_FWD, 4_000_000) == fa.FA_OK
+    try:
+        t0 = time.time()
+        call()
+        torch.cuda.synchronize()
+        assert time.time() - t0 < 2
+    finally:
+        fa.fa_debug_set_stall(0, 0)
+    call()                               # leaves at once: the word is set
+    with pytest.raises(fa.FaError) as e:
+        cache.check()
+    assert e.value.status == fa.FA_ERR_TIMEOUT
+    cache.check()
+    o, lse = call()
+    check(o, lse, q, dense, lens, 0, "bf16", 1 / math.sqrt(d))
