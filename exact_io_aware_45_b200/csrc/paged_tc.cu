@@ -15,9 +15,10 @@
 // a TMA box ends with its page, and at 16 tokens a page the boxes of one 128-key tile cost
 // their issuing thread 6,900 cycles, twice what the tile's products and softmax take).
 // They are written in the 128-byte swizzled layout of the MMA descriptors: 64-column
-// block cb at 16 KB * cb, row r at 128 r, 16-byte chunk c at c ^ (r & 7). A
-// tile is handed over once its copies have landed and a proxy fence has
-// made them visible to the tensor core.
+// block cb at 16 KB * cb, row r at 128 r, 16-byte chunk c at c ^ (r & 7). Each
+// copying thread's arrival on a tile's barrier is tied to its copies, so loaders never
+// wait for data, only for free slots; the MMA thread orders the landed bytes before
+// its reads with a proxy fence.
 //
 // The running maximum is a reference that moves only when a tile exceeds it by 2^8 (the
 // recurrence holds for any reference), so most tiles leave the accumulator alone.
@@ -63,6 +64,7 @@ struct Control {
   uint64_t done, never;
   uint32_t tmem;
   int abort, skip;
+  sched::Walk walk[8];                   // of the softmax warps, out of their registers
 };
 
 // Position of a tile in the order of loading and use, from the piece's first: two
@@ -82,12 +84,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const char* src, int bytes)
                "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
+// Arrives on `bar` (whose count includes it) when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void copy_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int D, bool kTwo>
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!sched::begin(a, pre, blockIdx.x, w)) return;      // the same answer in every warp
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < kSlots; ++i) {
-      mbar_init(&s.kv_full[i], kLoaders);
+      mbar_init(&s.kv_full[i], kLoaders * 32);
       mbar_init(&s.kv_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -142,16 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------ loaders
     const int me = warp == 0 ? 0 : warp - 1;
-    uint32_t n = 0, told = 0;                            // tiles issued, and handed over
-    // hands over the tiles below `to`, whose copies this warp has waited for
-    auto tell = [&](uint32_t to) {
-      if (to <= told) return;
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (uint32_t i = told; i < to; ++i) mbar_arrive(&s.kv_full[i % kSlots]);
-      told = to;
-    };
+    uint32_t n = 0;                                      // tiles issued
     bool ok = true;
     while (ok && w.x < w.end) {
       const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
@@ -159,6 +153,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tiles = pc.t1 - pc.t0;
       const long long head = (long long)pc.h * a.c.head_bytes;
       const int last = pc.hi > pc.lo ? (pc.hi - 1) >> a.c.page_log2 : -1;
+      // lane i looks up the page of keys 16 i .. 16 i + 15 of a tile (pages hold 16 keys or
+      // more), one tile ahead
+      auto look_up = [&](uint32_t j) {
+        const int e = ((pc.t0 + (int)j) * kN + (lane & 7) * 16) >> a.c.page_log2;
+        const int page = e <= last ? __ldg(trow + e) : 0;
+        return (unsigned)page < (unsigned)a.c.pages ? page : 0;
+      };
+      int page_n = look_up(0), page_k = 0, page_v = 0;   // of the next K, the last K, the next V
       for (uint32_t i = 0; i < 2 * tiles; ++i, ++n) {
         // the i-th tile in order of use: which of K and V, and its index
         uint32_t j;
@@ -170,52 +172,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           j = is_v ? (i + 1 == 2 * tiles ? tiles - 1 : i / 2 - 1) : (i + 1) / 2;
         }
         const uint32_t slot = n % kSlots;
-        if (n >= kSlots) {
-          uint64_t* bar = &s.kv_empty[slot];
-          const uint32_t parity = ((n / kSlots) & 1) ^ 1;
-          // before blocking, everything loaded is handed over: the tensor core may need it
-          // to get to the tile that frees this slot
-          if (!__all_sync(~0u, mbar_try_wait(bar, parity))) {
-            copy_wait<0>();
-            tell(n);
-            if (!__all_sync(~0u, wait(bar, parity))) {
-              ok = false;
-              break;
-            }
-          }
+        if (n >= kSlots && !__all_sync(~0u, wait(&s.kv_empty[slot], ((n / kSlots) & 1) ^ 1))) {
+          ok = false;
+          break;
         }
         const uint32_t to = smem_u32(base + C::kOffKV + slot * C::kTileBytes);
         const int j0 = (pc.t0 + (int)j) * kN;
         const char* from = is_v ? a.V : a.K;
-        // lane i knows the page of keys j0 + 16 i .. (pages hold 16 keys or more)
-        int page = 0;
-        {
-          const int e = (j0 + (lane & 7) * 16) >> a.c.page_log2;
-          if (e <= last) page = __ldg(trow + e);
-          if ((unsigned)page >= (unsigned)a.c.pages) page = 0;
+        if (!is_v) {
+          page_v = page_k;
+          page_k = page_n;
+          page_n = look_up(j + 1);
         }
+        // V_j follows K_j, or (one query tile, but for the last) K_{j+1}
+        const int page = is_v && !kTwo && j + 1 < tiles ? page_v : page_k;
         const bool edge = j0 < pc.lo || j0 + kN > pc.hi;
         constexpr int kVecs = D / 8, kRows = 32 / kVecs;  // chunks of a row; rows of an instruction
-        const int c = lane % kVecs;
-#pragma unroll 4
-        for (int r0 = me * kRows; r0 < kN; r0 += kLoaders * kRows) {
-          const int r = r0 + lane / kVecs;
-          const int pg = __shfl_sync(~0u, page, r0 >> 4);
+        constexpr int kGroup = 16 / kRows;               // instructions for 16 keys
+        const int c = lane % kVecs, rl = lane / kVecs;
+        // 16 keys of a head and page are contiguous: the loaders take them in turn
+        for (int g = me; g < kN / 16; g += kLoaders) {
+          const int pg = __shfl_sync(~0u, page, g);
           const char* src = from + pg * a.c.page_stride + head +
-                            (long long)((j0 + r) & ((1 << a.c.page_log2) - 1)) * (D * 2) + c * 16;
-          // rows that no query sees are not read and count as zero
-          const int bytes = edge && (j0 + r < pc.lo || j0 + r >= pc.hi) ? 0 : 16;
-          copy16(to + (c >> 3) * C::kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, bytes);
+                            (long long)((j0 + g * 16) & ((1 << a.c.page_log2) - 1)) * (D * 2) +
+                            lane * 16;
+          const uint32_t dst = to + (c >> 3) * C::kBlock + g * 16 * 128;
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            const int r = i * kRows + rl, j = j0 + g * 16 + r;
+            // rows that no query sees are not read and count as zero
+            const int bytes = edge && (j < pc.lo || j >= pc.hi) ? 0 : 16;
+            copy16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + i * 512, bytes);
+          }
         }
-        copy_commit();
-        if (n >= 2) {
-          copy_wait<2>();
-          tell(n - 1);
-        }
+        copy_arrive(&s.kv_full[slot]);
       }
     }
-    copy_wait<0>();
-    if (ok) tell(n);
+    copy_wait_all();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -225,7 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk0 = sdesc_sw128(smem_u32(base + C::kOffKV), 16, 1024);
       const uint64_t dv0 = sdesc_sw128(smem_u32(base + C::kOffKV), C::kBlock, 1024);
       auto slot_of = [&](uint32_t n) { return n % kSlots; };
-      auto have = [&](uint32_t n) { return wait(&s.kv_full[slot_of(n)], (n / kSlots) & 1); };
+      auto have = [&](uint32_t n) {
+        const bool got = wait(&s.kv_full[slot_of(n)], (n / kSlots) & 1);
+        fence_async_smem();
+        return got;
+      };
       auto release = [&](uint32_t n) { mma_commit(&s.kv_empty[slot_of(n)]); };
       // S_t = Q K^T with the tile at ring position n
       auto issue_s = [&](int t, uint32_t n) {
@@ -337,8 +334,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const stage = base + C::kOffStage + t * C::kStage;
     const int tid = threadIdx.x - 128 - t * 128;
     uint32_t cnt = 0;                                    // this warpgroup's tiles so far
-    for (uint32_t np = 0; w.x < w.end; ++np) {
-      const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+    bool more = true;
+    if (lane == 0) s.walk[warp - 4] = w;
+    __syncwarp();
+    for (uint32_t np = 0; more; ++np) {
+      sched::Walk v = s.walk[warp - 4];
+      const sched::Piece pc = sched::next(a, pre, blockIdx.x, v);
+      more = v.x < v.end;
+      __syncwarp();
+      if (lane == 0) s.walk[warp - 4] = v;
+      __syncwarp();
       const int ri = kTwo ? t * kM + r : r;              // row of the item
       sched::Row row;
       row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
