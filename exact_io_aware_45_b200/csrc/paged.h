@@ -41,11 +41,11 @@ cudaError_t cache_compact(const CacheView& c, void* ws, cudaStream_t st);
 size_t cache_workspace_bytes(int pages, int slots, int n);
 
 // One phase of an attention call: `items` row tiles (of up to `rows` packed
-// query rows that share a KV head), each over its own key tiles of `tile` keys, cut
+// query rows that share a KV head), each over its own key tiles, cut
 // into even ranges for `n` streams (paged_sched.cuh).
 struct Phase {
   int rows = 0;        // query rows per item, at most
-  int tile = 0;        // keys per tile
+  int tile_log2 = 0;   // keys per tile = 1 << tile_log2
   int rt = 0;          // row tiles per (sequence, KV head); per KV head in the shared phase
   int n = 0;           // streams
   int items = 0;
@@ -73,17 +73,48 @@ struct PagedArgs {
   Phase own, pre;
 };
 
+// Launches a kernel of a call's chain (shared phase, own phase, join). With `after`
+// it may start before the kernel ahead of it in the stream has finished, once that
+// has let it (chain_next); it then has to wait (chain_wait) before it reads that
+// kernel's results, or before it ends if it reads none: the end of the chain's last
+// kernel implies the end of all.
+template <class... P, class... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                           cudaStream_t st, bool after, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void chain_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void chain_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
 // Kernel families. Each runs one phase (`pre`: the shared prefix).
 cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
-constexpr int kSimtRows = 8, kSimtTile = 32, kSimtBlocksPerSm = 4;
+constexpr int kSimtRows = 8, kSimtTileLog2 = 5, kSimtBlocksPerSm = 4;
 // mma.sync kernel for few packed rows (bf16, d in {64, 128}); a stream is a warp.
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
 constexpr int kMmaMaxRows = 16, kMmaWarps = 8;
-constexpr int mma_tile(int d) { return d == 128 ? 16 : 32; }
+constexpr int mma_tile_log2(int d) { return d == 128 ? 4 : 5; }
 // tcgen05 kernel for many packed rows (bf16, d in {64, 128}); a stream is a CTA.
 // fold = 2: one query tile of 128 rows, its key tiles dealt to two warpgroups.
 cudaError_t paged_tc(const PagedArgs& a, bool pre, cudaStream_t st);
-constexpr int kTcTile = 128, kTcRows = 128;
+constexpr int kTcTileLog2 = 7, kTcRows = 128;
 // Joins the partial results of both phases.
 cudaError_t paged_join(const PagedArgs& a, int dtype, cudaStream_t st);
 

@@ -99,18 +99,18 @@ Phase divide(const CacheView& v, int groups, int rows, int sms) {
   switch (family(v, rows)) {
     case kSimt:
       p.rows = kSimtRows;
-      p.tile = kSimtTile;
+      p.tile_log2 = kSimtTileLog2;
       p.n = sms * kSimtBlocksPerSm;
       break;
     case kMma:
       p.rows = rows <= 8 ? 8 : kMmaMaxRows;
-      p.tile = mma_tile(v.d);
+      p.tile_log2 = mma_tile_log2(v.d);
       p.n = sms * kMmaWarps;
       break;
     case kTc:
       p.fold = rows <= kTcRows ? 2 : 1;
       p.rows = p.fold == 2 ? kTcRows : 2 * kTcRows;
-      p.tile = kTcTile;
+      p.tile_log2 = kTcTileLog2;
       p.n = sms;
       p.over = 1;
       p.snap = 1;
@@ -150,8 +150,8 @@ fa_status check_fwd(const CacheView& v, int B, int T, int Hq, int shared) {
   if (B < 0 || T < 0 || Hq <= 0 || Hq % v.Hkv != 0 || shared < 0) return FA_ERR_INVALID_ARG;
   if (shared & ((1 << v.page_log2) - 1)) return FA_ERR_INVALID_ARG;
   if (shared > v.width << v.page_log2) return FA_ERR_INVALID_ARG;
-  // packed rows, items and table indexes stay in int
-  if ((long long)B * T * Hq >= (1ll << 28) || (long long)T * (Hq / v.Hkv) >= (1ll << 20))
+  // packed rows, items and table indexes stay in int, and the join's grid in its limits
+  if (B > 65535 || (long long)B * T * Hq >= (1ll << 28) || (long long)T * (Hq / v.Hkv) >= (1ll << 20))
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }

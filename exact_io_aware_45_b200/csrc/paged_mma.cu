@@ -108,7 +108,7 @@ struct Pages {
 template <int D, int NT>
 __global__ void __launch_bounds__(kMmaWarps * 32, 1)
     mma_kernel(const PagedArgs a, const bool pre) {
-  constexpr int kTile = mma_tile(D), kGroups = kTile / 16;   // 16 keys a group
+  constexpr int kTile = 1 << mma_tile_log2(D), kGroups = kTile / 16;   // 16 keys a group
   constexpr int kGroupBytes = 16 * D * 2;
   constexpr int kRowVecs = D / 8;                            // 16-byte chunks of a row
   extern __shared__ uint8_t smem_raw[];
@@ -117,8 +117,12 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1)
   const Phase& ph = pre ? a.pre : a.own;
   // neighbouring streams on different SMs: little work is spread over all of them
   const int stream = warp * gridDim.x + blockIdx.x;
+  chain_next();
   sched::Walk w;
-  if (!sched::begin(a, pre, stream, w)) return;
+  if (!sched::begin(a, pre, stream, w)) {
+    chain_wait();
+    return;
+  }
 
   const int gid = lane >> 2, tig = lane & 3;
   const uint32_t k_row = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
@@ -350,15 +354,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1)
     }
   }
   copy_wait<0>();
+  chain_wait();
 }
 
 template <int D, int NT>
 cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
   if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(mma_kernel<D, NT>), kSmem))
     return e;
-  mma_kernel<D, NT><<<(pre ? a.pre : a.own).n / kMmaWarps, kMmaWarps * 32, kSmem, st>>>(a, pre);
-  count_launch();
-  return cudaGetLastError();
+  return launch_chained(mma_kernel<D, NT>, (pre ? a.pre : a.own).n / kMmaWarps, kMmaWarps * 32,
+                        kSmem, st, !pre && a.shared, a, pre);
 }
 
 }  // namespace

@@ -45,7 +45,7 @@ __device__ __forceinline__ void own_keys(const PagedArgs& a, int len, int& lo, i
   if (a.wl >= 0) lo = max((long long)lo, (long long)len - a.T - a.wl);
 }
 __device__ __forceinline__ int units_of(const Phase& ph, int lo, int hi) {
-  return ph.over + (hi > lo ? (hi - 1) / ph.tile - lo / ph.tile + 1 : 1);
+  return ph.over + (hi > lo ? ((hi - 1) >> ph.tile_log2) - (lo >> ph.tile_log2) + 1 : 1);
 }
 __device__ __forceinline__ int own_units(const PagedArgs& a, int len) {
   int lo, hi;
@@ -100,25 +100,37 @@ __device__ __forceinline__ void pieces_of(const Phase& ph, int s, int u, const C
 }
 
 // The batch as one warp sees it: units of all sequences, those before sequence
-// `b`, the smallest and the largest length. All lanes call it.
+// `b`, the smallest and the largest length, and that of b. All lanes call it.
 struct Batch {
-  int W, before, least, most;
+  int W, before, least, most, len;
 };
 __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
-  Batch t{0, 0, 0x7fffffff, 0};
-  const int per_b = a.c.Hkv * a.own.rt;
-  for (int i = threadIdx.x & 31; i < a.B; i += 32) {
-    const int len = len_of(a, i);
-    const int u = own_units(a, len) * per_b;
-    t.W += u;
-    if (i < b) t.before += u;
-    t.least = min(t.least, len);
-    t.most = max(t.most, len);
+  Batch t{0, 0, 0x7fffffff, 0, 0};
+  const int per_b = a.c.Hkv * a.own.rt, lane = threadIdx.x & 31;
+  constexpr int kAtOnce = 4;                      // dependent loads in flight per lane
+  for (int i0 = lane; i0 < a.B; i0 += 32 * kAtOnce) {
+    int slot[kAtOnce], len[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) slot[k] = i0 + 32 * k < a.B ? slot_of(a, i0 + 32 * k) : -1;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) len[k] = len_at(a, slot[k]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= a.B) break;
+      const int u = own_units(a, len[k]) * per_b;
+      t.W += u;
+      if (i < b) t.before += u;
+      if (i == b) t.len = len[k];
+      t.least = min(t.least, len[k]);
+      t.most = max(t.most, len[k]);
+    }
   }
   t.W = __reduce_add_sync(~0u, t.W);
   t.before = __reduce_add_sync(~0u, t.before);
   t.least = __reduce_min_sync(~0u, t.least);
   t.most = __reduce_max_sync(~0u, t.most);
+  t.len = __reduce_max_sync(~0u, t.len);
   return t;
 }
 
@@ -234,7 +246,7 @@ struct Piece {
   int table;         // slot whose table names the keys (the first sequence's in the shared phase)
   int row0, rows;    // rows: (g, t) of sequence b, or (b, g, t) in the shared phase
   int lo, hi;        // keys in sight of any row
-  int t0, t1;        // key tiles [t0, t1), in units of `tile` keys from key 0
+  int t0, t1;        // key tiles [t0, t1), counted from key 0
   int slot;          // partial slot, or -1: write the result
 };
 
@@ -251,7 +263,7 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, int i, Walk&
   p.row0 = w.r * ph.rows;
   p.rows = min(ph.rows, (pre ? a.B * a.TG : a.TG) - p.row0);
   const int from = w.x - w.s, to = min(w.u, w.end - w.s);
-  const int base = w.lo / ph.tile;
+  const int base = w.lo >> ph.tile_log2;
   p.t0 = base + max(0, from - ph.over);
   p.t1 = base + to - ph.over;
   const bool alone = from == 0 && to == w.u && a.shared == 0 && ph.fold == 1;

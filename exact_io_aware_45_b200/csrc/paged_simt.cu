@@ -22,7 +22,7 @@ namespace fa {
 namespace {
 
 constexpr int kRows = kSimtRows;
-constexpr int kTile = kSimtTile;
+constexpr int kTile = 1 << kSimtTileLog2;
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -77,8 +77,12 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
   constexpr int kVec = 16 / (int)sizeof(T);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Phase& ph = pre ? a.pre : a.own;
+  chain_next();
   sched::Walk w;
-  if (!sched::begin(a, pre, blockIdx.x, w)) return;   // the block's warps walk alike
+  if (!sched::begin(a, pre, blockIdx.x, w)) {         // the block's warps walk alike
+    chain_wait();
+    return;
+  }
   const T* Q = static_cast<const T*>(a.Q);
   while (w.x < w.end) {
     const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
@@ -210,13 +214,13 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
       }
     }
   }
+  chain_wait();
 }
 
 template <typename T, int D>
 cudaError_t launch_simt(const PagedArgs& a, bool pre, cudaStream_t st) {
-  simt_kernel<T, D><<<(pre ? a.pre : a.own).n, kWarps * 32, 0, st>>>(a, pre);
-  count_launch();
-  return cudaGetLastError();
+  return launch_chained(simt_kernel<T, D>, (pre ? a.pre : a.own).n, kWarps * 32, 0, st,
+                        !pre && a.shared, a, pre);
 }
 
 template <typename T>
@@ -232,110 +236,124 @@ cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
 // ---------------------------------------------------------------- join
 
 // O = sum_p 2^(lse_p - lse) O_p, lse = log2 sum_p 2^lse_p over a row's partial
-// results, whose slots follow from the same arithmetic that cut them. A warp
-// has a row (kSplit = 1), or all warps of a block share one and meet in shared memory:
-// few rows have many pieces each (a long sequence is cut into hundreds), and one
-// warp would go through them for longer than the attention took. Reads (d + 1)
-// floats a piece and row, from L2 mostly.
+// results, whose slots follow from the same arithmetic that cut them. A block has
+// up to eight rows of a sequence and KV head; where it has fewer, several warps share a
+// row and meet in shared memory, since few rows have many pieces each (a long
+// sequence is cut into hundreds). One warp finds where the cuts are: with every warp
+// at it, a batch of 128 spent 20 us on the arithmetic alone. Reads (d + 1) floats a piece and row, from L2 mostly.
 constexpr int kJoinWarps = 8;
 
-template <typename T, int D, bool kShare>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
-  __shared__ float part_o[kShare ? kJoinWarps : 1][D], part_lse[kJoinWarps];
+  __shared__ float part_o[kJoinWarps][D], part_sum[kJoinWarps];
+  __shared__ sched::Batch batch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = kShare ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
-  if (row >= a.B * a.c.Hkv * a.TG) return;
-  const int bh = row / a.TG, q = row - bh * a.TG;
-  const int b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
-  const sched::Batch t = sched::scan_batch(a, b);
+  const int h = blockIdx.x, b = blockIdx.y;
+  if (warp == 0) {
+    const sched::Batch mine = sched::scan_batch(a, b);
+    if (lane == 0) batch = mine;
+  }
+  __syncthreads();
+  const sched::Batch t = batch;
   const sched::Cuts cuts(a.own, t.W);
-  const int u = sched::own_units(a, sched::len_of(a, b));
-  const int r = q / a.own.rows, in = h * a.own.rt + r;
-  int first, more, pre_first = 0, pre_more = -1, pre_item = 0, pre_row = 0;
-  sched::pieces_of(a.own, t.before + in * u, u, cuts, first, more);
+  const int u = sched::own_units(a, t.len);
+  int pu = 1;
   if (a.shared) {
     int lo, hi;
     sched::pre_keys(a, t.least, t.most, lo, hi);
-    const int pu = sched::units_of(a.pre, lo, hi), pr = b * a.TG + q;
-    pre_item = h * a.pre.rt + pr / a.pre.rows;
-    pre_row = pr % a.pre.rows;
-    sched::pieces_of(a.pre, pre_item * pu, pu, sched::Cuts(a.pre, a.pre.items * pu), pre_first,
-                     pre_more);
-  } else if (more == 0 && a.own.fold == 1) {
-    return;                                             // written by its only piece
+    pu = sched::units_of(a.pre, lo, hi);
   }
-  const int own_count = (more + 1) * a.own.fold;
-  const int count = own_count + (pre_more + 1) * a.pre.fold;
-  // row index of partial p in its phase's buffers
-  auto at_of = [&](int p) -> long long {
-    const bool own = p < own_count;
-    const Phase& ph = own ? a.own : a.pre;
-    if (!own) p -= own_count;
-    int f = 0;
-    if (ph.fold == 2) f = p & 1, p >>= 1;
-    const int slot = own ? (p == 0 ? b * a.c.Hkv * a.own.rt + in : a.own.items + first + p)
-                         : (p == 0 ? pre_item : a.pre.items + pre_first + p);
-    return ((long long)slot * ph.fold + f) * ph.rows + (own ? q - r * a.own.rows : pre_row);
-  };
-  float top = -INFINITY;
-  for (int p = lane; p < count; p += 32)
-    top = fmaxf(top, (p < own_count ? a.own.lse : a.pre.lse)[at_of(p)]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int p = kShare ? warp : 0; p < count; p += kShare ? kJoinWarps : 1) {
-    const long long at = at_of(p);
-    const float c = exp2f((p < own_count ? a.own.lse : a.pre.lse)[at] - ref);
-    sum += c;
-    if (lane * kPer < D) {
-      float v[kPer];
-      load_f<kPer>((p < own_count ? a.own.o : a.pre.o) + at * D + lane * kPer, v);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
+  const sched::Cuts pre_cuts(a.pre, max(1, a.pre.items) * pu);
+  // `ways` warps a row, the block's rows side by side
+  int ways = kJoinWarps;
+  while (ways > 1 && kJoinWarps / ways < a.TG) ways >>= 1;
+  const int side = kJoinWarps / ways, way = warp % ways;
+  chain_wait();                                         // the partial results are there
+  for (int q0 = blockIdx.z * kJoinWarps; q0 < min(a.TG, (int)(blockIdx.z + 1) * kJoinWarps);
+       q0 += side) {
+    const int q = q0 + warp / ways;
+    const int r = q / a.own.rows, in = h * a.own.rt + r;
+    int first = 0, more = 0, pre_first = 0, pre_more = -1, pre_item = 0, pre_row = 0;
+    bool mine = q < a.TG;
+    if (mine) {
+      sched::pieces_of(a.own, t.before + in * u, u, cuts, first, more);
+      if (a.shared) {
+        const int pr = b * a.TG + q;
+        pre_item = h * a.pre.rt + pr / a.pre.rows;
+        pre_row = pr % a.pre.rows;
+        sched::pieces_of(a.pre, pre_item * pu, pu, pre_cuts, pre_first, pre_more);
+      } else if (more == 0 && a.own.fold == 1) {
+        mine = false;                                   // written by its only piece
+      }
     }
-  }
-  if constexpr (kShare) {
-    if (lane * kPer < D)
+    const int own_count = (more + 1) * a.own.fold;
+    const int count = mine ? own_count + (pre_more + 1) * a.pre.fold : 0;
+    // row index of partial p in its phase's buffers
+    auto at_of = [&](int p) -> long long {
+      const bool own = p < own_count;
+      const Phase& ph = own ? a.own : a.pre;
+      if (!own) p -= own_count;
+      int f = 0;
+      if (ph.fold == 2) f = p & 1, p >>= 1;
+      const int slot = own ? (p == 0 ? b * a.c.Hkv * a.own.rt + in : a.own.items + first + p)
+                           : (p == 0 ? pre_item : a.pre.items + pre_first + p);
+      return ((long long)slot * ph.fold + f) * ph.rows + (own ? q - r * a.own.rows : pre_row);
+    };
+    float top = -INFINITY;
+    for (int p = lane; p < count; p += 32)
+      top = fmaxf(top, (p < own_count ? a.own.lse : a.pre.lse)[at_of(p)]);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
-    if (lane == 0) part_lse[warp] = sum;
-    __syncthreads();
-    if (warp) return;
-    sum = 0.f;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int p = way; p < count; p += ways) {
+      const long long at = at_of(p);
+      const float c = exp2f((p < own_count ? a.own.lse : a.pre.lse)[at] - ref);
+      sum += c;
+      if (lane * kPer < D) {
+        float v[kPer];
+        load_f<kPer>((p < own_count ? a.own.o : a.pre.o) + at * D + lane * kPer, v);
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) {
-      sum += part_lse[k];
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
+      }
+    }
+    if (ways > 1) {
+      __syncthreads();
       if (lane * kPer < D)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] += part_o[k][lane * kPer + e];
-    }
-  }
-  const size_t out = (size_t)(b * a.Hq + h * a.G) * a.T + q;
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  if (lane * kPer < D)
+        for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
+      if (lane == 0) part_sum[warp] = sum;
+      __syncthreads();
+      if (way) continue;
+      sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      store_f(static_cast<T*>(a.O) + out * D + lane * kPer + e, acc[e] * inv);
-  if (lane == 0) a.LSE[out] = (top + log2f(sum)) * 0.6931471805599453f;
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+      for (int k = 0; k < ways; ++k) {
+        sum += part_sum[warp + k];
+        if (lane * kPer < D)
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] += part_o[warp + k][lane * kPer + e];
+      }
+    }
+    if (!mine) continue;
+    const size_t out = (size_t)(b * a.Hq + h * a.G) * a.T + q;
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    if (lane * kPer < D)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        store_f(static_cast<T*>(a.O) + out * D + lane * kPer + e, acc[e] * inv);
+    if (lane == 0) a.LSE[out] = (top + log2f(sum)) * 0.6931471805599453f;
+  }
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, cudaStream_t st) {
-  const int rows = a.B * a.c.Hkv * a.TG;
-  // with fewer rows than warps on the device, a block per row keeps it busier
-  if (rows <= 1184)
-    join_kernel<T, D, true><<<rows, kJoinWarps * 32, 0, st>>>(a);
-  else
-    join_kernel<T, D, false><<<(rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st>>>(a);
-  count_launch();
-  return cudaGetLastError();
+  const dim3 grid(a.c.Hkv, a.B, (a.TG + kJoinWarps - 1) / kJoinWarps);
+  return launch_chained(join_kernel<T, D>, grid, kJoinWarps * 32, 0, st, true, a);
 }
 
 template <typename T>

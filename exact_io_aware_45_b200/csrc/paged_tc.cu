@@ -36,7 +36,7 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kLoaders = 3;            // warps 0, 2 and 3
-constexpr int kM = 128, kN = kTcTile;  // query rows and keys of a tile
+constexpr int kM = kTcRows, kN = 1 << kTcTileLog2;  // query rows and keys of a tile
 constexpr float kTau = 8.0f;           // slack of the reference maximum, log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -104,8 +104,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Phase& ph = pre ? a.pre : a.own;
+  chain_next();
   sched::Walk w;
-  if (!sched::begin(a, pre, blockIdx.x, w)) return;      // the same answer in every warp
+  if (!sched::begin(a, pre, blockIdx.x, w)) {            // the same answer in every warp
+    chain_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < kSlots; ++i) {
       mbar_init(&s.kv_full[i], kLoaders * 32);
@@ -135,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (s.skip) {                                          // nothing is in flight yet
     __syncthreads();
     if (warp == 2) tmem_dealloc(tm, 512);
+    chain_wait();
     return;
   }
   const Guard guard{&s.abort, a.c.err};
@@ -349,16 +354,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
       if (ri < pc.rows) row = sched::row_of(a, pre, pc, ri);
       {
-        // Q into its swizzled tile: this thread's row, or half of it
-        constexpr int kVecs = D / 8, kMine = kTwo ? kVecs : kVecs / 2;
-        const int4* from = reinterpret_cast<const int4*>(
-            static_cast<const __nv_bfloat16*>(a.Q) + (size_t)row.out * D);
-        uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + r * 128;
+        // this warp's rows of Q (or half of them) into the swizzled tile, whole rows at a time
+        constexpr int kVecs = D / 8, kRows = 32 / kVecs, kMine = kTwo ? 32 : 16;
+        constexpr int kLoads = kMine / kRows;
+        const int c = lane % kVecs, r0 = (kTwo ? 0 : t * 16) + lane / kVecs;
+        const int w0 = (warp & 3) * 32, top = kTwo ? t * kM : 0;
+        int4 x[kLoads];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int v = kTwo ? i : t * kMine + i;
-          const int4 x = ri < pc.rows ? __ldg(from + v) : make_int4(0, 0, 0, 0);
-          *reinterpret_cast<int4*>(to + (v >> 3) * C::kBlock + (((v & 7) ^ (r & 7)) << 4)) = x;
+        for (int i = 0; i < kLoads; ++i) {
+          const int rr = r0 + i * kRows, out = __shfl_sync(~0u, row.out, rr);
+          x[i] = make_int4(0, 0, 0, 0);
+          if (top + w0 + rr < pc.rows)
+            x[i] = __ldg(reinterpret_cast<const int4*>(static_cast<const __nv_bfloat16*>(a.Q) +
+                                                       (size_t)out * D) + c);
+        }
+        uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + (c >> 3) * C::kBlock;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int rr = w0 + r0 + i * kRows;
+          *reinterpret_cast<int4*>(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
         }
         fence_async_smem();
         __syncwarp();
@@ -505,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tm, 512);
   }
+  chain_wait();
 }
 
 template <int D, bool kTwo>
@@ -514,10 +529,8 @@ cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
   if (cudaError_t e =
           set_max_dynamic_smem(reinterpret_cast<const void*>(tc_kernel<D, kTwo>), C::kBytes))
     return e;
-  tc_kernel<D, kTwo><<<(pre ? a.pre : a.own).n, kThreads, C::kBytes, st>>>(
-      a, pre, debug_stall_cycles(kStallFwd));
-  count_launch();
-  return cudaGetLastError();
+  return launch_chained(tc_kernel<D, kTwo>, (pre ? a.pre : a.own).n, kThreads, C::kBytes, st,
+                        !pre && a.shared, a, pre, debug_stall_cycles(kStallFwd));
 }
 
 }  // namespace
