@@ -50,6 +50,8 @@ struct Phase {
   int n = 0;           // streams
   int items = 0;
   int fold = 1;        // partial results per piece and row
+  bool blocked = false;  // partial O lies as [128-row block][32 columns][row][32], with the
+                         // 16-byte chunk c of a row's 32 columns at c ^ (row & 7)
   int over = 4;        // units of an item beside its tiles
   int snap = 4;        // tiles that a cut keeps from an item's ends
   int least = 12;      // units that a stream is worth

@@ -109,6 +109,7 @@ Phase divide(const CacheView& v, int groups, int rows, int sms) {
       break;
     case kTc:
       p.fold = rows <= kTcRows ? 2 : 1;
+      p.blocked = true;
       p.rows = p.fold == 2 ? kTcRows : 2 * kTcRows;
       p.tile_log2 = kTcTileLog2;
       p.n = sms;
@@ -130,12 +131,14 @@ cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) 
   }
 }
 
-// Fills in both phases; false if their units do not fit an int.
+// Fills in both phases; false if their units or partial rows do not fit an int.
 bool plan(PagedArgs& a, int sms) {
   a.own = divide(a.c, a.B * a.c.Hkv, a.TG, sms);
   a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, sms) : Phase();
   const long long keys = (long long)a.c.width << a.c.page_log2;
   const long long most = keys / 16 + 8;
+  for (const Phase* p : {&a.own, &a.pre})
+    if (((long long)p->items + p->n) * p->rows * p->fold >= (1ll << 31)) return false;
   return a.own.items * most < (1ll << 31) - (1 << 20) &&
          a.pre.items * most < (1ll << 31) - (1 << 20);
 }

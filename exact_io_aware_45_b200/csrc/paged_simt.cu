@@ -237,98 +237,132 @@ cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
 
 // O = sum_p 2^(lse_p - lse) O_p, lse = log2 sum_p 2^lse_p over a row's partial
 // results, whose slots follow from the same arithmetic that cut them. A block has
-// up to eight rows of a sequence and KV head; where it has fewer, several warps share a
-// row and meet in shared memory, since few rows have many pieces each (a long
-// sequence is cut into hundreds). One warp finds where the cuts are: with every warp
-// at it, a batch of 128 spent 20 us on the arithmetic alone. Reads (d + 1) floats a piece and row, from L2 mostly.
+// `rows` rows of a sequence; where these are fewer than its warps, several warps share a
+// row and meet in shared memory (few rows have many pieces each: a long sequence
+// is cut into hundreds). Reads (d + 1) floats a piece and row, from L2 mostly, and is
+// bound by instructions: one warp does the arithmetic of the cuts, a lane per row (with
+// every warp at it, a batch of 128 spent 20 us there), and per piece a warp
+// issues two shuffles, a load and d / 32 multiply-adds.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinMaxRows = 16;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a, const int rows) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
+  struct RowPieces {
+    int own, own_head, own_next;   // partial results of the own phase, first slots
+    int all, pre_head, pre_next;   // of both phases
+    int own_row, pre_row;
+  };
   __shared__ float part_o[kJoinWarps][D], part_sum[kJoinWarps];
-  __shared__ sched::Batch batch;
+  __shared__ RowPieces info[kJoinMaxRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int b = blockIdx.y, in_b = a.c.Hkv * a.TG;
+  const int r0 = blockIdx.x * rows, count = min(rows, in_b - r0);
   if (warp == 0) {
-    const sched::Batch mine = sched::scan_batch(a, b);
-    if (lane == 0) batch = mine;
+    const sched::Batch t = sched::scan_batch(a, b);
+    if (lane < count) {
+      const int h = (r0 + lane) / a.TG, q = r0 + lane - h * a.TG;
+      const sched::Cuts cuts(a.own, t.W);
+      const int u = sched::own_units(a, t.len);
+      const int rt = q / a.own.rows, in = h * a.own.rt + rt;
+      int first, more;
+      sched::pieces_of(a.own, t.before + in * u, u, cuts, first, more);
+      RowPieces p;
+      p.own = (more + 1) * a.own.fold;
+      p.own_head = b * a.c.Hkv * a.own.rt + in;
+      p.own_next = a.own.items + first;
+      p.own_row = q - rt * a.own.rows;
+      p.all = p.own;
+      p.pre_head = p.pre_next = p.pre_row = 0;
+      if (a.shared) {
+        int lo, hi;
+        sched::pre_keys(a, t.least, t.most, lo, hi);
+        const int pu = sched::units_of(a.pre, lo, hi);
+        const int pr = b * a.TG + q, prt = pr / a.pre.rows;
+        p.pre_head = h * a.pre.rt + prt;
+        p.pre_row = pr - prt * a.pre.rows;
+        sched::pieces_of(a.pre, p.pre_head * pu, pu, sched::Cuts(a.pre, a.pre.items * pu), first,
+                         more);
+        p.pre_next = a.pre.items + first;
+        p.all += (more + 1) * a.pre.fold;
+      } else if (more == 0 && a.own.fold == 1) {
+        p.all = 0;                                      // written by its only piece
+      }
+      info[lane] = p;
+    }
   }
   __syncthreads();
-  const sched::Batch t = batch;
-  const sched::Cuts cuts(a.own, t.W);
-  const int u = sched::own_units(a, t.len);
-  int pu = 1;
-  if (a.shared) {
-    int lo, hi;
-    sched::pre_keys(a, t.least, t.most, lo, hi);
-    pu = sched::units_of(a.pre, lo, hi);
-  }
-  const sched::Cuts pre_cuts(a.pre, max(1, a.pre.items) * pu);
-  // `ways` warps a row, the block's rows side by side
-  int ways = kJoinWarps;
-  while (ways > 1 && kJoinWarps / ways < a.TG) ways >>= 1;
-  const int side = kJoinWarps / ways, way = warp % ways;
   chain_wait();                                         // the partial results are there
-  for (int q0 = blockIdx.z * kJoinWarps; q0 < min(a.TG, (int)(blockIdx.z + 1) * kJoinWarps);
-       q0 += side) {
-    const int q = q0 + warp / ways;
-    const int r = q / a.own.rows, in = h * a.own.rt + r;
-    int first = 0, more = 0, pre_first = 0, pre_more = -1, pre_item = 0, pre_row = 0;
-    bool mine = q < a.TG;
-    if (mine) {
-      sched::pieces_of(a.own, t.before + in * u, u, cuts, first, more);
-      if (a.shared) {
-        const int pr = b * a.TG + q;
-        pre_item = h * a.pre.rt + pr / a.pre.rows;
-        pre_row = pr % a.pre.rows;
-        sched::pieces_of(a.pre, pre_item * pu, pu, pre_cuts, pre_first, pre_more);
-      } else if (more == 0 && a.own.fold == 1) {
-        mine = false;                                   // written by its only piece
-      }
-    }
-    const int own_count = (more + 1) * a.own.fold;
-    const int count = mine ? own_count + (pre_more + 1) * a.pre.fold : 0;
-    // row index of partial p in its phase's buffers
-    auto at_of = [&](int p) -> long long {
-      const bool own = p < own_count;
+  // `ways` warps a row
+  int ways = kJoinWarps;
+  while (ways > 1 && ways * count > kJoinWarps) ways >>= 1;
+  const int way = warp & (ways - 1);
+  // shared rows are done in one go, all warps meeting below
+  const int stop = ways > 1 ? kJoinWarps / ways : count;
+  for (int i = warp / ways; i < stop; i += kJoinWarps / ways) {
+    RowPieces p;
+    p.all = 0;
+    if (i < count) p = info[i];
+    // row index of partial result k in its phase's buffers
+    auto at_of = [&](int k) {
+      const bool own = k < p.own;
       const Phase& ph = own ? a.own : a.pre;
-      if (!own) p -= own_count;
-      int f = 0;
-      if (ph.fold == 2) f = p & 1, p >>= 1;
-      const int slot = own ? (p == 0 ? b * a.c.Hkv * a.own.rt + in : a.own.items + first + p)
-                           : (p == 0 ? pre_item : a.pre.items + pre_first + p);
-      return ((long long)slot * ph.fold + f) * ph.rows + (own ? q - r * a.own.rows : pre_row);
+      if (!own) k -= p.own;
+      const int f = ph.fold == 2 ? k & 1 : 0;
+      k >>= ph.fold == 2 ? 1 : 0;
+      const int slot = k ? (own ? p.own_next : p.pre_next) + k : (own ? p.own_head : p.pre_head);
+      return (slot * ph.fold + f) * ph.rows + (own ? p.own_row : p.pre_row);
     };
-    float top = -INFINITY;
-    for (int p = lane; p < count; p += 32)
-      top = fmaxf(top, (p < own_count ? a.own.lse : a.pre.lse)[at_of(p)]);
+    float top = -INFINITY, lse = -INFINITY;             // lane k: of partial result k
+    int at = 0;
+    for (int k = lane; k < p.all; k += 32) {
+      at = at_of(k);
+      lse = (k < p.own ? a.own.lse : a.pre.lse)[at];
+      top = fmaxf(top, lse);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < p.all; k0 += 32) {
+      if (p.all > 32) {
+        lse = -INFINITY;
+        if (k0 + lane < p.all) {
+          at = at_of(k0 + lane);
+          lse = (k0 + lane < p.own ? a.own.lse : a.pre.lse)[at];
+        }
+      }
+      const float weight = exp2f(lse - ref);
+      const int n = min(32, p.all - k0), own = p.own - k0;
 #pragma unroll 4
-    for (int p = way; p < count; p += ways) {
-      const long long at = at_of(p);
-      const float c = exp2f((p < own_count ? a.own.lse : a.pre.lse)[at] - ref);
-      sum += c;
-      if (lane * kPer < D) {
-        float v[kPer];
-        load_f<kPer>((p < own_count ? a.own.o : a.pre.o) + at * D + lane * kPer, v);
+      for (int k = way; k < n; k += ways) {
+        const float c = __shfl_sync(~0u, weight, k);
+        const int row = __shfl_sync(~0u, at, k);
+        const Phase& ph = k < own ? a.own : a.pre;
+        const int col = lane * kPer;
+        const float* from = ph.o + (size_t)row * D + col;
+        if (ph.blocked)
+          from = ph.o + (size_t)(row >> 7) * (128 * D) + (col >> 5) * (128 * 32) +
+                 (row & 127) * 32 + ((((col >> 2) & 7) ^ (row & 7)) << 2) + (col & 3);
+        sum += c;
+        if (col < D) {
+          float v[kPer];
+          load_f<kPer>(from, v);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
+        }
       }
     }
     if (ways > 1) {
-      __syncthreads();
       if (lane * kPer < D)
 #pragma unroll
         for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
       if (lane == 0) part_sum[warp] = sum;
       __syncthreads();
-      if (way) continue;
+      if (way) return;
       sum = 0.f;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
@@ -339,7 +373,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
           for (int e = 0; e < kPer; ++e) acc[e] += part_o[warp + k][lane * kPer + e];
       }
     }
-    if (!mine) continue;
+    if (p.all == 0) continue;
+    const int h = (r0 + i) / a.TG, q = r0 + i - h * a.TG;
     const size_t out = (size_t)(b * a.Hq + h * a.G) * a.T + q;
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     if (lane * kPer < D)
@@ -352,8 +387,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
 
 template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, cudaStream_t st) {
-  const dim3 grid(a.c.Hkv, a.B, (a.TG + kJoinWarps - 1) / kJoinWarps);
-  return launch_chained(join_kernel<T, D>, grid, kJoinWarps * 32, 0, st, true, a);
+  // enough blocks for the device first, then rows that share a block's set-up
+  const long long all = (long long)a.B * a.c.Hkv * a.TG;
+  int rows = 1;
+  while (rows < kJoinMaxRows && all / (2 * rows) >= 300) rows *= 2;
+  const dim3 grid((a.c.Hkv * a.TG + rows - 1) / rows, a.B);
+  return launch_chained(join_kernel<T, D>, grid, kJoinWarps * 32, 0, st, true, a, rows);
 }
 
 template <typename T>

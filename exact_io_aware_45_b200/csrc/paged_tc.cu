@@ -89,6 +89,12 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// 16-byte aligned shared -> global bulk store.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -131,6 +137,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) {
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
+  }
+  // Softmax warps: row `r` of query tile t (of the one query tile). The first piece's Q
+  // is fetched here, ahead of the loaders' flood, the next ones' behind each piece.
+  const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+  const int item_row = kTwo ? t * kM + r : r;
+  sched::Piece pc;
+  sched::Row row;
+  auto fetch = [&] {
+    sched::Walk v = s.walk[warp - 4];
+    pc = sched::next(a, pre, blockIdx.x, v);
+    __syncwarp();
+    if (lane == 0) s.walk[warp - 4] = v;
+    __syncwarp();
+    row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
+    if (item_row < pc.rows) row = sched::row_of(a, pre, pc, item_row);
+    // this warp's rows of Q (or half of them) into the swizzled tile, whole rows at a time
+    constexpr int kVecs = D / 8, kRows = 32 / kVecs, kMine = kTwo ? 32 : 16;
+    constexpr int kLoads = kMine / kRows;
+    const int c = lane % kVecs, r0 = (kTwo ? 0 : t * 16) + lane / kVecs;
+    const int w0 = (warp & 3) * 32, top = kTwo ? t * kM : 0;
+    int4 x[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int rr = r0 + i * kRows, out = __shfl_sync(~0u, row.out, rr);
+      x[i] = make_int4(0, 0, 0, 0);
+      if (top + w0 + rr < pc.rows)
+        x[i] = __ldg(reinterpret_cast<const int4*>(static_cast<const __nv_bfloat16*>(a.Q) +
+                                                   (size_t)out * D) + c);
+    }
+    uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + (c >> 3) * C::kBlock;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int rr = w0 + r0 + i * kRows;
+      *reinterpret_cast<int4*>(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+    }
+    fence_async_smem();
+  };
+  if (warp >= 4) {
+    if (lane == 0) s.walk[warp - 4] = w;
+    __syncwarp();
+    fetch();
   }
   tc_fence_before();
   __syncthreads();
@@ -326,8 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = (warp - 4) >> 2;                       // warpgroup
-    const int r = (warp & 3) * 32 + lane;                // row of its query tile, TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_reg = tm + t * C::kS + lanes;
     const uint32_t o_reg = tm + C::kO + t * D + lanes;
@@ -339,45 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const stage = base + C::kOffStage + t * C::kStage;
     const int tid = threadIdx.x - 128 - t * 128;
     uint32_t cnt = 0;                                    // this warpgroup's tiles so far
-    bool more = true;
-    if (lane == 0) s.walk[warp - 4] = w;
-    __syncwarp();
-    for (uint32_t np = 0; more; ++np) {
-      sched::Walk v = s.walk[warp - 4];
-      const sched::Piece pc = sched::next(a, pre, blockIdx.x, v);
-      more = v.x < v.end;
+    auto have_q = [&] {                                  // what fetch() stored may be read
       __syncwarp();
-      if (lane == 0) s.walk[warp - 4] = v;
-      __syncwarp();
-      const int ri = kTwo ? t * kM + r : r;              // row of the item
-      sched::Row row;
-      row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
-      if (ri < pc.rows) row = sched::row_of(a, pre, pc, ri);
-      {
-        // this warp's rows of Q (or half of them) into the swizzled tile, whole rows at a time
-        constexpr int kVecs = D / 8, kRows = 32 / kVecs, kMine = kTwo ? 32 : 16;
-        constexpr int kLoads = kMine / kRows;
-        const int c = lane % kVecs, r0 = (kTwo ? 0 : t * 16) + lane / kVecs;
-        const int w0 = (warp & 3) * 32, top = kTwo ? t * kM : 0;
-        int4 x[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int rr = r0 + i * kRows, out = __shfl_sync(~0u, row.out, rr);
-          x[i] = make_int4(0, 0, 0, 0);
-          if (top + w0 + rr < pc.rows)
-            x[i] = __ldg(reinterpret_cast<const int4*>(static_cast<const __nv_bfloat16*>(a.Q) +
-                                                       (size_t)out * D) + c);
-        }
-        uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + (c >> 3) * C::kBlock;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int rr = w0 + r0 + i * kRows;
-          *reinterpret_cast<int4*>(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.q_full[kTwo ? t : 0]);
-      }
+      if (lane == 0) mbar_arrive(&s.q_full[kTwo ? t : 0]);
+    };
+    have_q();
+    for (uint32_t np = 0;; ++np) {
       const int lo_all = __reduce_max_sync(~0u, row.lo), hi_all = __reduce_min_sync(~0u, row.hi);
       float m_ref = -INFINITY, l = 0.f;
       bool first = true;
@@ -468,15 +480,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       const float lse2 = m_ref + log2f(l);
-      const long long at = (long long)pc.slot * (ph.rows * ph.fold) + t * kM;   // partial row 0
-      if (ri < pc.rows) {
-        if (pc.slot < 0) a.LSE[row.out] = lse2 * kLn2;
+      const int slot = pc.slot;
+      const long long at = (long long)slot * (ph.rows * ph.fold) + t * kM;   // partial row 0
+      if (item_row < pc.rows) {
+        if (slot < 0) a.LSE[row.out] = lse2 * kLn2;
         else ph.lse[at + r] = lse2;
       }
-      // rows through shared memory, 32 columns at a time, so that a warp writes lines
       const int rows = min(kM, kTwo ? pc.rows - t * kM : pc.rows);
       // of the tile's row 0 (own phase: the rows of a sequence and KV head are contiguous)
       const int out0 = (pc.b * a.Hq + pc.h * a.G) * a.T + pc.row0 + t * kM;
+      // the next piece's Q goes in before this one's result goes out, so that its first
+      // scores are computed meanwhile
+      const bool more = s.walk[warp - 4].x < s.walk[warp - 4].end;
+      if (more) {
+        fetch();
+        have_q();
+      }
+      // Rows through shared memory, 32 columns at a time: partial results as they lie there
+      // (the join knows the swizzle), 16 KB by one bulk store; results in whole lines.
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         uint32_t o[32];
@@ -486,31 +507,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
+        if (slot >= 0 && k > 0) {
+          if (tid == 0) bulk_wait_read0();
+          named_sync(1 + t, 128);
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           *reinterpret_cast<float4*>(stage + r * 128 + ((q ^ (r & 7)) << 4)) =
               make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
                           __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-        named_sync(1 + t, 128);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = i * 16 + (tid >> 3), q = tid & 7;
-          const float4 v =
-              *reinterpret_cast<const float4*>(stage + rr * 128 + ((q ^ (rr & 7)) << 4));
-          if (rr < rows) {
-            if (pc.slot < 0) {
-              __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.O) +
-                                  (size_t)(out0 + rr) * D + k * 32 + q * 4;
-              *reinterpret_cast<uint2*>(to) =
-                  make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-            } else {
-              *reinterpret_cast<float4*>(ph.o + (at + rr) * D + k * 32 + q * 4) = v;
-            }
+        if (slot >= 0) {
+          fence_async_smem();
+          named_sync(1 + t, 128);
+          if (tid == 0) {
+            bulk_store(ph.o + at * D + k * (kM * 32), stage, C::kStage);
+            bulk_commit();
           }
+        } else {
+          named_sync(1 + t, 128);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 16 + (tid >> 3), q = tid & 7;
+            const float4 v =
+                *reinterpret_cast<const float4*>(stage + rr * 128 + ((q ^ (rr & 7)) << 4));
+            if (rr < rows)
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) +
+                                        (size_t)(out0 + rr) * D + k * 32 + q * 4) =
+                  make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          }
+          named_sync(1 + t, 128);
         }
+      }
+      if (slot >= 0) {
+        if (tid == 0) bulk_wait_read0();
         named_sync(1 + t, 128);
       }
       tc_fence_before();
+      if (!more) break;
     }
   }
   tc_fence_before();
@@ -519,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tm, 512);
   }
+  if (threadIdx.x == 128 || threadIdx.x == 256) bulk_wait0();   // its partial results are written
   chain_wait();
 }
 
