@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "paged.h"
 
 namespace fa {
@@ -73,11 +75,15 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
   return FA_OK;
 }
 
+// SMs of the current device, asked for once per device.
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    n = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -113,9 +119,9 @@ Phase divide(const CacheView& v, int groups, int rows, int sms) {
       p.rows = p.fold == 2 ? kTcRows : 2 * kTcRows;
       p.tile_log2 = kTcTileLog2;
       p.n = sms;
-      p.over = 1;
+      p.over = 3;          // a further piece costs a stream 6 us, a tile 2 us
       p.snap = 1;
-      p.least = 3;
+      p.least = 5;
       break;
   }
   p.rt = (rows + p.rows - 1) / p.rows;

@@ -138,8 +138,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
-  // Softmax warps: row `r` of query tile t (of the one query tile). The first piece's Q
-  // is fetched here, ahead of the loaders' flood, the next ones' behind each piece.
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = s.tmem;
+  if (s.skip) {                                          // nothing is in flight yet
+    __syncthreads();
+    if (warp == 2) tmem_dealloc(tm, 512);
+    chain_wait();
+    return;
+  }
+  const Guard guard{&s.abort, a.c.err};
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_ready_first(bar, parity, guard);
+  };
+
+  // Softmax warps: row `r` of query tile t (of the one query tile), and the next piece's
+  // rows and Q.
   const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
   const int item_row = kTwo ? t * kM + r : r;
   sched::Piece pc;
@@ -173,25 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       *reinterpret_cast<int4*>(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
     }
     fence_async_smem();
-  };
-  if (warp >= 4) {
-    if (lane == 0) s.walk[warp - 4] = w;
-    __syncwarp();
-    fetch();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = s.tmem;
-  if (s.skip) {                                          // nothing is in flight yet
-    __syncthreads();
-    if (warp == 2) tmem_dealloc(tm, 512);
-    chain_wait();
-    return;
-  }
-  const Guard guard{&s.abort, a.c.err};
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait_ready_first(bar, parity, guard);
   };
 
   if (warp == 0 || warp == 2 || warp == 3) {
@@ -384,6 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const stage = base + C::kOffStage + t * C::kStage;
     const int tid = threadIdx.x - 128 - t * 128;
     uint32_t cnt = 0;                                    // this warpgroup's tiles so far
+    if (lane == 0) s.walk[warp - 4] = w;
+    __syncwarp();
+    fetch();
     auto have_q = [&] {                                  // what fetch() stored may be read
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.q_full[kTwo ? t : 0]);

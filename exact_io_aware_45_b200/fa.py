@@ -519,22 +519,6 @@ def attention(q, k, v, scale: Optional[float] = None, causal: bool = False, bloc
 
 # ------------------------------------------------------------------ paged cache
 
-class _on:
-    """Makes a tensor's device current, where it is not."""
-
-    def __init__(self, device):
-        import torch
-        self.to = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.to is not None:
-            self.to.__enter__()
-
-    def __exit__(self, *exc):
-        if self.to is not None:
-            self.to.__exit__(*exc)
-
-
 class PagedCache:
     """Keys and values of many sequences in a pool of fixed-size pages (fa_cache
     of include/fa.h, which says what the calls do and when they are refused).
@@ -568,6 +552,11 @@ class PagedCache:
                           _dtype_code(k.dtype), _ptr(table), _ptr(lens), _ptr(refs),
                           table.shape[0], table.shape[1], _ptr(self.err))
         self._ref = ctypes.byref(self._c)
+        # a call costs the host as much as small ones cost the GPU: what every call needs is
+        # looked up once (workspace sizes by the sizes they depend on)
+        self._torch, self._lib, self._index = torch, lib(), k.device.index
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._sizes = {}
         if fa_cache_workspace_size(self._ref, 0) == 0:
             raise ValueError("unsupported cache: page_size is 16, 32, 64 or 128, d 16, 32, 64 or "
                              "128, strides are multiples of 16 bytes")
@@ -584,124 +573,144 @@ class PagedCache:
         lens, refs = (torch.zeros(n, dtype=torch.int32, device=device) for n in (seqs, pages))
         return cls(k, v, table, lens, refs)
 
-    def _list(self, *tensors):
-        import torch
-        for t in tensors:
-            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
-                    t.device != self.device:
-                raise ValueError("a list is a contiguous int32 tensor on the cache's device")
-            if t.numel() != tensors[0].numel():
-                raise ValueError("lists of different lengths")
-        return tensors[0].numel()
+    def _list(self, t) -> int:
+        """The length of a list of slots, pages, positions or offsets."""
+        if t.dtype is not self._torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+                t.get_device() != self._index:
+            raise ValueError("a list is a contiguous int32 tensor on the cache's device")
+        return t.numel()
 
-    def _workspace(self, n: int):
-        import torch
-        return torch.empty(fa_cache_workspace_size(self._ref, n), dtype=torch.uint8,
-                           device=self.device)
+    def _call(self, name, *args):
+        """A library call on the cache's device and its current stream."""
+        cuda = self._torch.cuda
+        fn = getattr(self._lib, name)
+        if cuda.current_device() == self._index:
+            s = fn(self._ref, *args, self._raw_stream(self._index))
+        else:
+            with cuda.device(self._index):
+                s = fn(self._ref, *args, self._raw_stream(self._index))
+        if s != FA_OK:
+            raise FaError(s, name)
 
-    def _stream(self):
-        import torch
-        return torch.cuda.current_stream(self.device).cuda_stream
+    def _empty(self, size, dtype):
+        return self._torch.empty(size, dtype=dtype, device=self.device)
+
+    def _workspace(self, *key):
+        """A new workspace: for lists of (n,) entries, or attention of (B, T, Hq, shared)."""
+        size = self._sizes.get(key)
+        if size is None:
+            fn = fa_cache_workspace_size if len(key) == 1 else fa_paged_workspace_size
+            with self._torch.cuda.device(self._index):
+                size = self._sizes[key] = fn(self._ref, *key)
+        return self._empty(size, self._torch.uint8), size
 
     def extend(self, seqs, tokens):
         """Makes room for new tokens: `tokens` of each sequence, or cu_seqlens
         (int32 [n + 1]). Returns the positions of the first ones, int32 [n]."""
-        import torch
         n = self._list(seqs)
-        cu = None
+        cu, each = 0, tokens       # (a list stays referenced until its use is enqueued)
         if not isinstance(tokens, int):
             if self._list(tokens) != n + 1:
                 raise ValueError("cu_seqlens has one entry more than the list of sequences")
-            cu, tokens = tokens, 0
-        with _on(self.device):
-            pos = torch.empty_like(seqs)
-            ws = self._workspace(n)
-            _check(fa_cache_extend(self._ref, _ptr(seqs), n, _ptr(cu), tokens, _ptr(pos), _ptr(ws),
-                                   ws.numel(), self._stream()), "fa_cache_extend")
+            cu, each = tokens.data_ptr(), 0
+        pos = self._empty(n, self._torch.int32)
+        ws, size = self._workspace(n)
+        self._call("fa_cache_extend", seqs.data_ptr(), n, cu, each, pos.data_ptr(),
+                   ws.data_ptr(), size)
         return pos
 
     def write(self, layer: int, k, v, seqs, pos, cu_seqlens=None):
         """Writes new keys and values [total, Hkv, d] of one layer from the
         positions that extend returned on; rows of equal shares, or cu_seqlens."""
-        n = self._list(seqs, pos)
-        if cu_seqlens is not None and self._list(cu_seqlens) != n + 1:
-            raise ValueError("cu_seqlens has one entry more than the list of sequences")
+        n = self._list(seqs)
+        if self._list(pos) != n:
+            raise ValueError("lists of different lengths")
+        cu = 0
+        if cu_seqlens is not None:
+            if self._list(cu_seqlens) != n + 1:
+                raise ValueError("cu_seqlens has one entry more than the list of sequences")
+            cu = cu_seqlens.data_ptr()
+        shape = k.shape
         for t in (k, v):
-            if t.dim() != 3 or t.shape[1:] != (self.Hkv, self.d) or t.dtype != self.dtype or \
-                    not t.is_contiguous() or t.device != self.device or t.shape != k.shape:
+            if t.shape != shape or t.dtype != self.dtype or not t.is_contiguous() or \
+                    t.get_device() != self._index:
                 raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
-        with _on(self.device):
-            _check(fa_cache_write(self._ref, layer, _ptr(k), _ptr(v), _ptr(seqs), _ptr(pos), n,
-                                  _ptr(cu_seqlens), k.shape[0], self._stream()), "fa_cache_write")
+        if len(shape) != 3 or shape[1] != self.Hkv or shape[2] != self.d:
+            raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
+        self._call("fa_cache_write", layer, k.data_ptr(), v.data_ptr(), seqs.data_ptr(),
+                   pos.data_ptr(), n, cu, shape[0])
 
-    def _op(self, name, fn, *lists):
-        n = self._list(*lists)
-        with _on(self.device):
-            ws = self._workspace(n)
-            _check(fn(self._ref, *map(_ptr, lists), n, _ptr(ws), ws.numel(), self._stream()), name)
+    def _pairs(self, name, src, dst):
+        n = self._list(src)
+        if self._list(dst) != n:
+            raise ValueError("lists of different lengths")
+        ws, size = self._workspace(n)
+        self._call(name, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), size)
 
     def fork(self, src, dst):
         """Makes the empty sequences dst copies of src: full pages are shared."""
-        self._op("fa_cache_fork", fa_cache_fork, src, dst)
-
-    def free(self, seqs):
-        """Empties sequences and gives up their pages."""
-        self._op("fa_cache_free", fa_cache_free, seqs)
+        self._pairs("fa_cache_fork", src, dst)
 
     def copy_pages(self, src, dst):
         """Copies pages src to pages dst in all layers."""
-        self._op("fa_cache_copy", fa_cache_copy, src, dst)
+        self._pairs("fa_cache_copy", src, dst)
+
+    def free(self, seqs):
+        """Empties sequences and gives up their pages."""
+        n = self._list(seqs)
+        ws, size = self._workspace(n)
+        self._call("fa_cache_free", seqs.data_ptr(), n, ws.data_ptr(), size)
 
     def compact(self):
         """Moves the pages in use to the front of the pool."""
-        with _on(self.device):
-            ws = self._workspace(0)
-            _check(fa_cache_compact(self._ref, _ptr(ws), ws.numel(), self._stream()),
-                   "fa_cache_compact")
+        ws, size = self._workspace(0)
+        self._call("fa_cache_compact", ws.data_ptr(), size)
 
     def check(self):
         """Raises FaError if the device refused a call since the last check
         (synchronises the stream)."""
-        with _on(self.device):
-            _check(fa_get_device_error(_ptr(self.err), self._stream()), "paged cache")
+        with self._torch.cuda.device(self._index):
+            _check(fa_get_device_error(_ptr(self.err), self._raw_stream(self._index)),
+                   "paged cache")
 
 
 def _forward_cache(q, cache, layer, shared, seqs, scale, causal, window_left, softcap, out, lse,
                    workspace):
-    import torch
-    if q.dim() != 4 or q.dtype != cache.dtype or q.device != cache.device or \
-            not q.is_contiguous() or q.shape[3] != cache.d:
+    index, shape = cache._index, q.shape
+    if q.dtype != cache.dtype or q.get_device() != index or not q.is_contiguous() or \
+            len(shape) != 4 or shape[3] != cache.d:
         raise ValueError("q is a contiguous [B, Hq, T, d] of the cache's type, on its device")
-    B, Hq, T, d = q.shape
+    B, Hq, T, d = shape
     if seqs is not None and cache._list(seqs) != B:
         raise ValueError("one sequence for each batch entry")
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or
-                            out.device != q.device or not out.is_contiguous()):
+    torch = cache._torch
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != shape or out.dtype != q.dtype or out.get_device() != index or \
+            not out.is_contiguous():
         raise ValueError("out is like q")
-    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or
-                            lse.device != q.device or not lse.is_contiguous()):
+    if lse is None:
+        lse = cache._empty((B, Hq, T), torch.float32)
+    elif lse.shape != shape[:3] or lse.dtype != torch.float32 or lse.get_device() != index or \
+            not lse.is_contiguous():
         raise ValueError("lse is float32 [B, Hq, T]")
+    if workspace is None:
+        workspace, size = cache._workspace(B, T, Hq, shared)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace is contiguous, on the cache's device")
+    else:
+        size = workspace.numel() * workspace.element_size()
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with _on(cache.device):
-        o = torch.empty_like(q) if out is None else out
-        l = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(fa_paged_workspace_size(cache._ref, B, T, Hq, shared),
-                             dtype=torch.uint8, device=q.device)
-        elif ws.device != q.device or not ws.is_contiguous():
-            raise ValueError("workspace is contiguous, on the cache's device")
-        nbytes = ws.numel() * ws.element_size()
-        if shared:
-            _check(fa_fwd_shared(cache._ref, layer, _ptr(q), _ptr(o), _ptr(l), _ptr(seqs), B, T,
-                                 Hq, shared, scale, int(bool(causal)), window_left, softcap,
-                                 _ptr(ws), nbytes, cache._stream()), "fa_fwd_shared")
-        else:
-            _check(fa_fwd_paged(cache._ref, layer, _ptr(q), _ptr(o), _ptr(l), _ptr(seqs), B, T, Hq,
-                                scale, int(bool(causal)), window_left, softcap, _ptr(ws), nbytes,
-                                cache._stream()), "fa_fwd_paged")
-    return o, l
+        scale = d ** -0.5
+    slots = 0 if seqs is None else seqs.data_ptr()
+    causal = 1 if causal else 0
+    if shared:
+        cache._call("fa_fwd_shared", layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), slots, B,
+                    T, Hq, shared, scale, causal, window_left, softcap, workspace.data_ptr(), size)
+    else:
+        cache._call("fa_fwd_paged", layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), slots, B, T,
+                    Hq, scale, causal, window_left, softcap, workspace.data_ptr(), size)
+    return out, lse
 
 
 def forward_paged(q, cache: PagedCache, layer: int, seqs=None, scale: Optional[float] = None,
