@@ -53,8 +53,8 @@ struct Phase {
   bool blocked = false;  // partial O lies as [128-row block][32 columns][row][32], with the
                          // 16-byte chunk c of a row's 32 columns at c ^ (row & 7)
   int over = 4;        // units of an item beside its tiles
-  int snap = 4;        // tiles that a cut keeps from an item's ends
-  int least = 12;      // units that a stream is worth
+  int snap = 2;        // tiles that a cut keeps from an item's ends
+  int least = 4;       // units that a stream is worth
   float* o = nullptr;  // partial results: [items + n][fold][rows][d], normalised
   float* lse = nullptr;  // [items + n][fold][rows], base 2
 };
@@ -111,7 +111,7 @@ cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st)
 constexpr int kSimtRows = 8, kSimtTileLog2 = 5, kSimtBlocksPerSm = 4;
 // mma.sync kernel for few packed rows (bf16, d in {64, 128}); a stream is a warp.
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
-constexpr int kMmaMaxRows = 16, kMmaWarps = 8;
+constexpr int kMmaMaxRows = 16, kMmaWarps = 4, kMmaBlocksPerSm = 2;
 constexpr int mma_tile_log2(int d) { return d == 128 ? 4 : 5; }
 // tcgen05 kernel for many packed rows (bf16, d in {64, 128}); a stream is a CTA.
 // fold = 2: one query tile of 128 rows, its key tiles dealt to two warpgroups.

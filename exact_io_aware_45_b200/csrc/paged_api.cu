@@ -98,10 +98,11 @@ Family family(const CacheView& v, int rows) {
 }
 
 // The work division of a phase of `groups` sequences and KV heads with `rows`
-// packed rows each. It depends on sizes and types only, so the workspace query
-// and the call agree.
-Phase divide(const CacheView& v, int groups, int rows, int sms) {
+// packed rows each, over `keys` keys at most. It depends on sizes and types only, so the
+// workspace query and the call agree.
+Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) {
   Phase p;
+  int per = 1;           // streams of a block
   switch (family(v, rows)) {
     case kSimt:
       p.rows = kSimtRows;
@@ -111,7 +112,8 @@ Phase divide(const CacheView& v, int groups, int rows, int sms) {
     case kMma:
       p.rows = rows <= 8 ? 8 : kMmaMaxRows;
       p.tile_log2 = mma_tile_log2(v.d);
-      p.n = sms * kMmaWarps;
+      per = kMmaWarps;
+      p.n = sms * kMmaWarps * kMmaBlocksPerSm;
       break;
     case kTc:
       p.fold = rows <= kTcRows ? 2 : 1;
@@ -126,6 +128,10 @@ Phase divide(const CacheView& v, int groups, int rows, int sms) {
   }
   p.rt = (rows + p.rows - 1) / p.rows;
   p.items = groups * p.rt;
+  // no more streams than the longest sequences could use
+  const long long units = p.items * ((keys >> p.tile_log2) + 2 + p.over);
+  const long long most = units / p.least + per;
+  if (most < p.n) p.n = (int)(most / per * per);
   return p;
 }
 
@@ -139,9 +145,9 @@ cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) 
 
 // Fills in both phases; false if their units or partial rows do not fit an int.
 bool plan(PagedArgs& a, int sms) {
-  a.own = divide(a.c, a.B * a.c.Hkv, a.TG, sms);
-  a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, sms) : Phase();
   const long long keys = (long long)a.c.width << a.c.page_log2;
+  a.own = divide(a.c, a.B * a.c.Hkv, a.TG, keys, sms);
+  a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, a.shared, sms) : Phase();
   const long long most = keys / 16 + 8;
   for (const Phase* p : {&a.own, &a.pre})
     if (((long long)p->items + p->n) * p->rows * p->fold >= (1ll << 31)) return false;

@@ -5,7 +5,7 @@
 // A stream is a warp: it walks its share of the key tiles (paged_sched.cuh) with a
 // ring of three 8 KB stages of its own (16 keys of d = 128 or 32 of d = 64), filled
 // with cp.async and swizzled on the way (16-byte chunk c of a row goes to c ^ (row
-// & 7), so that the eight rows of an ldmatrix hit different banks). Eight warps an
+// & 7), so that the eight rows of an ldmatrix hit different banks). Two blocks of four warps an
 // SM keep up to 128 KB of loads in flight (at 6.5 TB/s over 148 SMs and ~1 us of
 // latency 45 KB would do). Warps never meet: no barrier, no merge in shared memory. A
 // first form with one TMA producer per SM and a merge per piece ran a ragged
@@ -106,7 +106,7 @@ struct Pages {
 
 // NT: n-tiles of eight packed query rows.
 template <int D, int NT>
-__global__ void __launch_bounds__(kMmaWarps * 32, 1)
+__global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
     mma_kernel(const PagedArgs a, const bool pre) {
   constexpr int kTile = 1 << mma_tile_log2(D), kGroups = kTile / 16;   // 16 keys a group
   constexpr int kGroupBytes = 16 * D * 2;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1)
   const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
 
   while (w.x < w.end) {
-    const sched::Piece pc = sched::next(a, pre, stream, w);
+    const sched::Piece pc = sched::next(a, pre, w);
     Pages pages;
     pages.open(sched::table_row(a, pc.table), (pc.t0 * kTile) >> a.c.page_log2,
                pc.hi > pc.lo ? (pc.hi - 1) >> a.c.page_log2 : -1);
@@ -163,12 +163,6 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1)
         }
       }
     };
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-      if (pc.t0 + i < pc.t1) load(pc.t0 + i);
-      copy_commit();
-    }
-
     // lane r keeps row r
     sched::Row row;
     row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
@@ -197,112 +191,116 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1)
         for (int i = 0; i < 4; ++i) o[n][k][i] = 0.f;
     }
 
-    for (int t = pc.t0; t < pc.t1; ++t) {
-      const uint32_t kb = ring + (uint32_t)(t - pc.t0) % kStages * kStageBytes;
-      const uint32_t vb = kb + kStageBytes / 2;
-      const int j0 = t * kTile;
-      copy_wait<kStages - 1>();
-      __syncwarp();
-      // two chains of products a group, for latency
-      float x[kGroups][NT][4], y[kGroups][NT][4];
+    // one loop for filling the ring and working from it: code that runs once is slow (its
+    // instructions come from L2)
+    for (int t = pc.t0 - kStages; t < pc.t1; ++t) {
+      if (t >= pc.t0) {
+        const uint32_t kb = ring + (uint32_t)(t - pc.t0) % kStages * kStageBytes;
+        const uint32_t vb = kb + kStageBytes / 2;
+        const int j0 = t * kTile;
+        copy_wait<kStages - 1>();
+        __syncwarp();
+        // two chains of products a group, for latency
+        float x[kGroups][NT][4], y[kGroups][NT][4];
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[g][n][i] = y[g][n][i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          uint32_t f[4];
-          ldsm4(f, kb + g * kGroupBytes + (k / 4) * 2048 + k_row +
-                       ((((k % 4) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma16816(k & 1 ? y[g][n] : x[g][n], f, qf[n][k][0], qf[n][k][1]);
-        }
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
+            for (int i = 0; i < 4; ++i) x[g][n][i] = y[g][n][i] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float z = x[g][n][i] + y[g][n][i];
-            if (a.softcap > 0.f) z = cap2 * tanh_ex2(z * to_cap);
-            else z *= scale2;
-            x[g][n][i] = z;
+          for (int g = 0; g < kGroups; ++g) {
+            uint32_t f[4];
+            ldsm4(f, kb + g * kGroupBytes + (k / 4) * 2048 + k_row +
+                         ((((k % 4) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(k & 1 ? y[g][n] : x[g][n], f, qf[n][k][0], qf[n][k][1]);
           }
-      if (j0 < lo_all || j0 + kTile > hi_all) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float z = x[g][n][i] + y[g][n][i];
+              if (a.softcap > 0.f) z = cap2 * tanh_ex2(z * to_cap);
+              else z *= scale2;
+              x[g][n][i] = z;
+            }
+        if (j0 < lo_all || j0 + kTile > hi_all) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int lo = __shfl_sync(~0u, row.lo, n * 8 + tig * 2 + i);
+              const int hi = __shfl_sync(~0u, row.hi, n * 8 + tig * 2 + i);
+#pragma unroll
+              for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = j0 + g * 16 + gid + e * 8;
+                  if (j < lo || j >= hi) x[g][n][i + 2 * e] = -INFINITY;
+                }
+            }
+        }
+        bool moved = false;
+        float corr[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int lo = __shfl_sync(~0u, row.lo, n * 8 + tig * 2 + i);
-            const int hi = __shfl_sync(~0u, row.hi, n * 8 + tig * 2 + i);
+            float top = fmaxf(x[0][n][i], x[0][n][i + 2]);
+            if constexpr (kGroups == 2) top = fmaxf(top, fmaxf(x[1][n][i], x[1][n][i + 2]));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+            top = fmaxf(top, m[n][i]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            moved |= top > m[n][i];
+            corr[n][i] = ex2(m[n][i] - ref);
+            m[n][i] = top;
+            float sum = 0.f;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int j = j0 + g * 16 + gid + e * 8;
-                if (j < lo || j >= hi) x[g][n][i + 2 * e] = -INFINITY;
+                const float p = ex2(x[g][n][i + 2 * e] - ref);
+                x[g][n][i + 2 * e] = p;
+                sum += p;
               }
+            l[n][i] = l[n][i] * corr[n][i] + sum;
           }
-      }
-      bool moved = false;
-      float corr[NT][2];
+        if (__any_sync(~0u, moved)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float top = fmaxf(x[0][n][i], x[0][n][i + 2]);
-          if constexpr (kGroups == 2) top = fmaxf(top, fmaxf(x[1][n][i], x[1][n][i + 2]));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-          top = fmaxf(top, m[n][i]);
-          const float ref = top == -INFINITY ? 0.f : top;
-          moved |= top > m[n][i];
-          corr[n][i] = ex2(m[n][i] - ref);
-          m[n][i] = top;
-          float sum = 0.f;
+            for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p = ex2(x[g][n][i + 2 * e] - ref);
-              x[g][n][i + 2 * e] = p;
-              sum += p;
-            }
-          l[n][i] = l[n][i] * corr[n][i] + sum;
+              for (int i = 0; i < 4; ++i) o[n][k][i] *= corr[n][i & 1];
         }
-      if (__any_sync(~0u, moved)) {
+        uint32_t pf[kGroups][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][k][i] *= corr[n][i & 1];
+            for (int e = 0; e < 2; ++e)
+              pf[g][n][e] = transpose8x8(pack_bf16(x[g][n][2 * e], x[g][n][2 * e + 1]));
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t f[4];
+            ldsm4t(f, vb + g * kGroupBytes + (k / 4) * 2048 + v_row +
+                          ((((k % 4) * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k], f, pf[g][n][0], pf[g][n][1]);
+          }
+        __syncwarp();
       }
-      uint32_t pf[kGroups][NT][2];
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            pf[g][n][e] = transpose8x8(pack_bf16(x[g][n][2 * e], x[g][n][2 * e + 1]));
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t f[4];
-          ldsm4t(f, vb + g * kGroupBytes + (k / 4) * 2048 + v_row +
-                        ((((k % 4) * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(o[n][k], f, pf[g][n][0], pf[g][n][1]);
-        }
-      __syncwarp();
       if (t + kStages < pc.t1) load(t + kStages);
       copy_commit();
     }

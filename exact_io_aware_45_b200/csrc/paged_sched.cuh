@@ -70,15 +70,12 @@ struct Cuts {
     each = W / n;
     extra = W - each * n;
   }
+  // where range i begins
   __device__ int at(int i) const { return i * each + min(i, extra); }
-  // the first cut at x or behind, and the last cut at x or before
+  // the first cut at x or behind
   __device__ int first(int x) const {
     const int y = x - extra * (each + 1);
     return y <= 0 ? (x + each) / (each + 1) : extra + (y + each - 1) / each;
-  }
-  __device__ int last(int x) const {
-    const int y = x - extra * (each + 1);
-    return y < 0 ? x / (each + 1) : extra + y / each;
   }
 };
 
@@ -96,16 +93,17 @@ __device__ __forceinline__ void pieces_of(const Phase& ph, int s, int u, const C
   first = more = 0;
   if (b < a) return;
   first = c.first(a) - 1;
-  more = max(0, c.last(b) - first);
+  more = c.first(b + 1) - 1 - first;
 }
 
 // The batch as one warp sees it: units of all sequences, those before sequence
 // `b`, the smallest and the largest length, and that of b. All lanes call it.
 struct Batch {
   int W, before, least, most, len;
+  int lane_len;      // of sequence `lane`
 };
 __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
-  Batch t{0, 0, 0x7fffffff, 0, 0};
+  Batch t{0, 0, 0x7fffffff, 0, 0, 0};
   const int per_b = a.c.Hkv * a.own.rt, lane = threadIdx.x & 31;
   constexpr int kAtOnce = 4;                      // dependent loads in flight per lane
   for (int i0 = lane; i0 < a.B; i0 += 32 * kAtOnce) {
@@ -114,6 +112,7 @@ __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
     for (int k = 0; k < kAtOnce; ++k) slot[k] = i0 + 32 * k < a.B ? slot_of(a, i0 + 32 * k) : -1;
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) len[k] = len_at(a, slot[k]);
+    if (i0 == lane) t.lane_len = len[0];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int i = i0 + 32 * k;
@@ -137,6 +136,7 @@ __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
 // A stream's way through its units.
 struct Walk {
   int x, end;        // next unit, and the first that is not its own
+  int stream;
   int s, u;          // first unit and units of the current item
   int item;          // (b * Hkv + h) * rt + row tile; (h * rt + row tile) in the shared phase
   int b, h, r;       // sequence (own phase), KV head, row tile
@@ -170,11 +170,12 @@ __device__ __forceinline__ void advance(const PagedArgs& a, Walk& w) {
   w.u = units_of(a.own, w.lo, w.hi);
 }
 
-// Sets up the walk of stream `i`; all lanes of a warp call it and get the same.
+// Sets up the walk of a stream; all lanes of a warp call it and get the same.
 // Returns false if the stream has no units.
 __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
   const int lane = threadIdx.x & 31;
   const Batch t = scan_batch(a, 0);
+  w.stream = i;
   if (pre) {
     pre_keys(a, t.least, t.most, w.lo, w.hi);
     w.u = units_of(a.pre, w.lo, w.hi);
@@ -200,7 +201,7 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
   int at0 = 0, b0 = -1, base = 0;
   w.end = x1 == c.W ? c.W : -1;
   for (int g = 0; g < a.B && (b0 < 0 || w.end < 0); g += 32) {
-    const int u = g + lane < a.B ? own_units(a, len_of(a, g + lane)) : 0;
+    const int u = g + lane < a.B ? own_units(a, g ? len_of(a, g + lane) : t.lane_len) : 0;
     int to = u * per_b;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -251,7 +252,7 @@ struct Piece {
 };
 
 // The next piece of the walk (w.x < w.end), which it moves past.
-__device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, int i, Walk& w) {
+__device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, Walk& w) {
   const Phase& ph = pre ? a.pre : a.own;
   Piece p;
   p.h = w.h;
@@ -267,7 +268,7 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, int i, Walk&
   p.t0 = base + max(0, from - ph.over);
   p.t1 = base + to - ph.over;
   const bool alone = from == 0 && to == w.u && a.shared == 0 && ph.fold == 1;
-  p.slot = alone ? -1 : (from == 0 ? w.item : ph.items + i);
+  p.slot = alone ? -1 : (from == 0 ? w.item : ph.items + w.stream);
   w.x = w.s + to;
   if (w.x < w.end) {
     w.s = w.x;

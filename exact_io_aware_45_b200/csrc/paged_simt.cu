@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
   }
   const T* Q = static_cast<const T*>(a.Q);
   while (w.x < w.end) {
-    const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+    const sched::Piece pc = sched::next(a, pre, w);
     __syncthreads();
     if (tid < kRows) {
       sched::Row r;

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sched::Row row;
   auto fetch = [&] {
     sched::Walk v = s.walk[warp - 4];
-    pc = sched::next(a, pre, blockIdx.x, v);
+    pc = sched::next(a, pre, v);
     __syncwarp();
     if (lane == 0) s.walk[warp - 4] = v;
     __syncwarp();
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0;                                      // tiles issued
     bool ok = true;
     while (ok && w.x < w.end) {
-      const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+      const sched::Piece pc = sched::next(a, pre, w);
       const int* trow = sched::table_row(a, pc.table);
       const uint32_t tiles = pc.t1 - pc.t0;
       const long long head = (long long)pc.h * a.c.head_bytes;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = injected_stall(&s.never, stall, guard);
       uint32_t n0 = 0;
       for (uint32_t np = 0; ok && w.x < w.end; ++np) {
-        const sched::Piece pc = sched::next(a, pre, blockIdx.x, w);
+        const sched::Piece pc = sched::next(a, pre, w);
         const uint32_t tiles = pc.t1 - pc.t0;
         if (kTwo) {
           // the K tile serves both query tiles; warpgroup 1 runs half a tile behind
