@@ -6,9 +6,9 @@
 // cache as it was) and hands out free pages lowest first, so its result does
 // not depend on timing: with f_p = 1 for a free page p, the k-th new page is
 // the p with f_p = 1 and sum_{q < p} f_q = k. Plans touch little data (4
-// bytes a page, 4 bytes a table entry) and are bound by latency: one cluster of
-// eight CTAs, which can synchronise between the steps of a plan without
-// another launch and shares the scan over the pages through distributed shared
+// bytes a page, 4 bytes a table entry) and are bound by latency: a plan is one block, or for
+// large pools one cluster of eight, which can synchronise between the steps of a plan
+// without another launch and shares the scan over the pages through distributed shared
 // memory.
 //
 // The data kernels move bytes and nothing else (16-byte loads and stores, 4 KB
@@ -23,9 +23,19 @@ namespace cg = cooperative_groups;
 namespace fa {
 namespace {
 
-constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 512;
-constexpr int kPlanAll = kPlanCtas * kPlanThreads;
+
+// The threads of a plan: kCtas blocks (one, or a cluster).
+template <int kCtas>
+struct Plan {
+  static constexpr int kAll = kCtas * kPlanThreads;
+  static __device__ int rank() { return kCtas > 1 ? (int)blockIdx.x : 0; }
+  static __device__ int thread() { return rank() * kPlanThreads + threadIdx.x; }
+  static __device__ void sync() {
+    if constexpr (kCtas > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  }
+};
 
 // Workspace of a plan, in int32 words: header, one bit per slot or page, one
 // prefix sum per list entry, two page lists and a page map.
@@ -94,12 +104,11 @@ __device__ int block_scan(int v, PlanShared& s, int& total) {
 }
 
 // Zeroes the header and the bits; everyone sees them afterwards.
+template <class P>
 __device__ void plan_begin(const PlanWs& p, int bits) {
-  cg::cluster_group cl = cg::this_cluster();
-  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
-  if (t == 0) *p.bad = 0, *p.count = 0;
-  for (int i = t; i < bits; i += kPlanAll) p.bits[i] = 0;
-  cl.sync();
+  if (P::thread() == 0) *p.bad = 0, *p.count = 0;
+  for (int i = P::thread(); i < bits; i += P::kAll) p.bits[i] = 0;
+  P::sync();
 }
 
 // Sets bit i; true if it was set already.
@@ -114,26 +123,31 @@ __device__ __forceinline__ bool in_range(int i, int n) { return (unsigned)i < (u
 
 // Calls emit(rank, i) for every i in [0, n) with pred(i), rank counting from 0 in
 // the order of i, for ranks below `limit`; returns how many i there are. The
-// whole cluster takes part; each CTA has a contiguous part of the range.
-template <class Pred, class Emit>
-__device__ int cluster_pick(int n, int limit, PlanShared& s, Pred pred, Emit emit) {
-  cg::cluster_group cl = cg::this_cluster();
+// whole plan takes part; each block has a contiguous part of the range.
+template <int kCtas, class Pred, class Emit>
+__device__ int plan_pick(int n, int limit, PlanShared& s, Pred pred, Emit emit) {
+  using P = Plan<kCtas>;
   constexpr int kPer = 4;
-  const int per = ((n + kPlanCtas - 1) / kPlanCtas + kPer - 1) / kPer * kPer;
-  const int lo = min(n, (int)blockIdx.x * per), hi = min(n, lo + per);
+  const int per = ((n + kCtas - 1) / kCtas + kPer - 1) / kPer * kPer;
+  const int lo = min(n, P::rank() * per), hi = min(n, lo + per);
   int mine = 0;
+#pragma unroll 4
   for (int i = lo + threadIdx.x; i < hi; i += kPlanThreads) mine += pred(i) ? 1 : 0;
   int total;
   block_scan(mine, s, total);
-  if (threadIdx.x == 0) s.mine = total;
-  cl.sync();
-  int before = 0, all = 0;
-  for (int r = 0; r < kPlanCtas; ++r) {
-    const int v = *cl.map_shared_rank(&s.mine, r);
-    if (r < (int)blockIdx.x) before += v;
-    all += v;
+  int before = 0, all = total;
+  if constexpr (kCtas > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (threadIdx.x == 0) s.mine = total;
+    cl.sync();
+    all = 0;
+    for (int r = 0; r < kCtas; ++r) {
+      const int v = *cl.map_shared_rank(&s.mine, r);
+      if (r < P::rank()) before += v;
+      all += v;
+    }
+    cl.sync();
   }
-  cl.sync();
   for (int base = lo; base < hi && before < limit; base += kPlanThreads * kPer) {
     const int i0 = base + threadIdx.x * kPer;
     bool f[kPer];
@@ -156,10 +170,10 @@ __device__ int cluster_pick(int n, int limit, PlanShared& s, Pred pred, Emit emi
 }
 
 // at[i] = sum of need(i') for i' < i, at[n] = the sum of all, saturated at 2^30.
-// The first CTA does it; the others meet it at the next cluster barrier.
-template <class Need>
+// The first block does it; the others meet it at the next barrier of the plan.
+template <class P, class Need>
 __device__ void list_scan(int n, int* at, PlanShared& s, Need need) {
-  if (blockIdx.x == 0) {
+  if (P::rank() == 0) {
     int base = 0;
     for (int b = 0; b < n; b += kPlanThreads) {
       const int i = b + threadIdx.x;
@@ -180,15 +194,16 @@ __device__ __forceinline__ int new_tokens(const int* cu, int tokens, int i) {
   return cu ? cu[i + 1] - cu[i] : tokens;
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kCtas>
+__global__ void __launch_bounds__(kPlanThreads)
     extend_kernel(CacheView c, const int* seqs, int n, const int* cu, int tokens, int* pos,
                   PlanWs p) {
   __shared__ PlanShared s;
-  cg::cluster_group cl = cg::this_cluster();
-  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  using P = Plan<kCtas>;
+  const int t = P::thread();
   const int ps = 1 << c.page_log2;
   const long long most = (long long)c.width * ps;
-  plan_begin(p, bit_words(0, c.slots));
+  plan_begin<P>(p, bit_words(0, c.slots));
   // sequence i: its slot, length and new tokens; false if any is wrong
   auto get = [&](int i, int& slot, int& len, int& more) {
     slot = seqs[i];
@@ -202,25 +217,25 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (!get(i, slot, len, more)) return 0;
     return ((len + more + ps - 1) >> c.page_log2) - ((len + ps - 1) >> c.page_log2);
   };
-  for (int i = t; i < n; i += kPlanAll) {
+  for (int i = t; i < n; i += P::kAll) {
     int slot, len, more;
     if (!get(i, slot, len, more) || set_bit(p.bits, slot)) *p.bad = 1;
   }
-  list_scan(n, p.at, s, need);
-  cl.sync();
+  list_scan<P>(n, p.at, s, need);
+  P::sync();
   const int total = __ldcg(p.at + n);
   int found = 0;
   if (total > 0 && total <= c.pages)
-    found = cluster_pick(c.pages, total, s, [&](int i) { return __ldcg(c.refs + i) == 0; },
+    found = plan_pick<kCtas>(c.pages, total, s, [&](int i) { return __ldcg(c.refs + i) == 0; },
                          [&](int k, int i) { p.to[k] = i; });
   const bool bad = __ldcg(p.bad) || found < total;
-  cl.sync();   // the lists are complete, and everyone has read what follows changes
+  P::sync();   // the lists are complete, and everyone has read what follows changes
   if (bad) {
-    for (int i = t; i < n; i += kPlanAll) pos[i] = -1;
+    for (int i = t; i < n; i += P::kAll) pos[i] = -1;
     if (t == 0) refuse(c);
     return;
   }
-  for (int k = t; k < total; k += kPlanAll) {
+  for (int k = t; k < total; k += P::kAll) {
     int a = 0, b = n - 1;   // the sequence that the k-th new page belongs to
     while (a < b) {
       const int m = (a + b + 1) >> 1;
@@ -231,8 +246,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     c.table[(size_t)slot * c.width + have + k - __ldcg(p.at + a)] = page;
     c.refs[page] = 1;
   }
-  cl.sync();
-  for (int i = t; i < n; i += kPlanAll) {
+  P::sync();
+  for (int i = t; i < n; i += P::kAll) {
     const int slot = seqs[i], len = __ldcg(c.lens + slot);
     pos[i] = len;
     c.lens[slot] = len + new_tokens(cu, tokens, i);
@@ -247,7 +262,9 @@ __global__ void __launch_bounds__(256)
     write_kernel(CacheView c, char* lk, char* lv, const char* K, const char* V, const int* seqs,
                  const int* pos, int n, const int* cu, int total) {
   const int lane = threadIdx.x & 31;
-  const int row_vecs = c.row_bytes >> 4;              // 16-byte pieces of a head's row
+  constexpr int kAtOnce = 4;                          // loads of K and of V a lane in flight
+  const int row_vecs = c.row_bytes >> 4;              // 16-byte pieces of a head's row (2^n)
+  const int row_log2 = 31 - __clz(row_vecs);
   const int vecs = c.Hkv * row_vecs;
   const int ps_mask = (1 << c.page_log2) - 1;
   const int warps = gridDim.x * (blockDim.x >> 5);
@@ -283,14 +300,23 @@ __global__ void __launch_bounds__(256)
       continue;
     }
     const size_t dst0 = (size_t)page * c.page_stride + (size_t)(at & ps_mask) * c.row_bytes;
-    const size_t src0 = (size_t)r * c.Hkv * c.row_bytes;
-    for (int v = lane; v < vecs; v += 32) {
-      const int h = v / row_vecs;
-      const size_t dst = dst0 + (size_t)h * c.head_bytes + (size_t)(v - h * row_vecs) * 16;
-      const int4 x = __ldcs(reinterpret_cast<const int4*>(K + src0) + v);
-      const int4 y = __ldcs(reinterpret_cast<const int4*>(V + src0) + v);
-      *reinterpret_cast<int4*>(lk + dst) = x;
-      *reinterpret_cast<int4*>(lv + dst) = y;
+    const int4* k = reinterpret_cast<const int4*>(K + (size_t)r * c.Hkv * c.row_bytes);
+    const int4* v = reinterpret_cast<const int4*>(V + (size_t)r * c.Hkv * c.row_bytes);
+    for (int v0 = lane; v0 < vecs; v0 += 32 * kAtOnce) {
+      int4 x[kAtOnce], y[kAtOnce];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (v0 + 32 * e < vecs) x[e] = __ldcs(k + v0 + 32 * e), y[e] = __ldcs(v + v0 + 32 * e);
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int i = v0 + 32 * e;
+        if (i < vecs) {
+          const int h = i >> row_log2;
+          const size_t dst = dst0 + (size_t)h * c.head_bytes + (size_t)(i & (row_vecs - 1)) * 16;
+          *reinterpret_cast<int4*>(lk + dst) = x[e];
+          *reinterpret_cast<int4*>(lv + dst) = y[e];
+        }
+      }
     }
   }
 }
@@ -331,62 +357,66 @@ __device__ void copy_pages(const CacheView& c, const int* from, const int* to, i
 
 __global__ void __launch_bounds__(256) copy_kernel(CacheView c, PlanWs p, const int* from,
                                                    const int* to, int n) {
+  chain_wait();
   if (*p.bad) return;
   copy_pages(c, from, to, n);
 }
 
 // ---------------------------------------------------------------- fork
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kCtas>
+__global__ void __launch_bounds__(kPlanThreads)
     fork_plan_kernel(CacheView c, const int* src, const int* dst, int n, PlanWs p) {
+  chain_next();
   __shared__ PlanShared s;
-  cg::cluster_group cl = cg::this_cluster();
-  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  using P = Plan<kCtas>;
+  const int t = P::thread();
   const int ps = 1 << c.page_log2;
   const long long most = (long long)c.width * ps;
-  plan_begin(p, bit_words(0, c.slots));
-  for (int i = t; i < n; i += kPlanAll) {
+  plan_begin<P>(p, bit_words(0, c.slots));
+  for (int i = t; i < n; i += P::kAll) {
     const int d = dst[i];
     if (!in_range(d, c.slots) || set_bit(p.bits, d) || c.lens[d] != 0) *p.bad = 1;
   }
-  cl.sync();
+  P::sync();
   // a partly filled last page needs a copy of its own
   auto need = [&](int i) {
     const int a = src[i];
     return in_range(a, c.slots) && (c.lens[a] & (ps - 1)) ? 1 : 0;
   };
-  for (int i = t; i < n; i += kPlanAll) {
+  for (int i = t; i < n; i += P::kAll) {
     const int a = src[i];
     if (!in_range(a, c.slots) || get_bit(p.bits, a) || c.lens[a] < 0 || c.lens[a] > most)
       *p.bad = 1;
   }
-  list_scan(n, p.at, s, need);
-  cl.sync();
+  list_scan<P>(n, p.at, s, need);
+  P::sync();
   const int total = __ldcg(p.at + n);
   int found = 0;
   if (total > 0 && total <= c.pages)
-    found = cluster_pick(c.pages, total, s, [&](int i) { return c.refs[i] == 0; },
+    found = plan_pick<kCtas>(c.pages, total, s, [&](int i) { return c.refs[i] == 0; },
                          [&](int k, int i) { p.to[k] = i; });
   if (!__ldcg(p.bad) && found >= total) {
-    for (int i = t; i < n; i += kPlanAll)
+    for (int i = t; i < n; i += P::kAll)
       if (need(i)) {
         const int a = src[i];
         p.from[p.at[i]] = c.table[(size_t)a * c.width + (c.lens[a] >> c.page_log2)];
       }
     if (t == 0) *p.count = total;
   } else {
-    cl.sync();   // every CTA has read `bad` before it is set for want of pages
+    P::sync();   // every CTA has read `bad` before it is set for want of pages
     if (t == 0) {
       *p.bad = 1;
       refuse(c);
     }
     return;
   }
-  cl.sync();
+  P::sync();
 }
 
 __global__ void __launch_bounds__(256)
     fork_kernel(CacheView c, const int* src, const int* dst, int n, PlanWs p) {
+  chain_wait();
   if (*p.bad) return;
   const int ps = 1 << c.page_log2;
   const long long all = (long long)gridDim.x * blockDim.x;
@@ -411,22 +441,23 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- free
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kCtas>
+__global__ void __launch_bounds__(kPlanThreads)
     free_kernel(CacheView c, const int* seqs, int n, PlanWs p) {
-  cg::cluster_group cl = cg::this_cluster();
-  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
-  plan_begin(p, bit_words(0, c.slots));
-  for (int i = t; i < n; i += kPlanAll) {
+  using P = Plan<kCtas>;
+  const int t = P::thread();
+  plan_begin<P>(p, bit_words(0, c.slots));
+  for (int i = t; i < n; i += P::kAll) {
     const int slot = seqs[i];
     if (!in_range(slot, c.slots) || set_bit(p.bits, slot)) *p.bad = 1;
   }
-  cl.sync();
+  P::sync();
   if (__ldcg(p.bad)) {
     if (t == 0) refuse(c);
     return;
   }
   const long long entries = (long long)n * c.width;
-  for (long long e = t; e < entries; e += kPlanAll) {
+  for (long long e = t; e < entries; e += P::kAll) {
     const int i = (int)(e / c.width), w = (int)(e - (long long)i * c.width);
     const int slot = seqs[i];
     int* at = c.table + (size_t)slot * c.width + w;
@@ -439,43 +470,47 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 
 // ---------------------------------------------------------------- copy
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kCtas>
+__global__ void __launch_bounds__(kPlanThreads)
     copy_plan_kernel(CacheView c, const int* src, const int* dst, int n, PlanWs p) {
-  cg::cluster_group cl = cg::this_cluster();
-  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
-  plan_begin(p, bit_words(c.pages, 0));
-  for (int i = t; i < n; i += kPlanAll) {
+  chain_next();
+  using P = Plan<kCtas>;
+  const int t = P::thread();
+  plan_begin<P>(p, bit_words(c.pages, 0));
+  for (int i = t; i < n; i += P::kAll) {
     const int d = dst[i];
     if (!in_range(d, c.pages) || set_bit(p.bits, d)) *p.bad = 1;
   }
-  cl.sync();
-  for (int i = t; i < n; i += kPlanAll) {
+  P::sync();
+  for (int i = t; i < n; i += P::kAll) {
     const int a = src[i];
     if (!in_range(a, c.pages) || get_bit(p.bits, a)) *p.bad = 1;
   }
-  cl.sync();
+  P::sync();
   if (t == 0 && __ldcg(p.bad)) refuse(c);
 }
 
 // ---------------------------------------------------------------- compact
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kCtas>
+__global__ void __launch_bounds__(kPlanThreads)
     compact_plan_kernel(CacheView c, PlanWs p) {
+  chain_next();
   __shared__ PlanShared s;
-  cg::cluster_group cl = cg::this_cluster();
-  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
-  plan_begin(p, 0);
-  const int live = cluster_pick(c.pages, 0, s, [&](int i) { return c.refs[i] > 0; },
+  using P = Plan<kCtas>;
+  const int t = P::thread();
+  plan_begin<P>(p, 0);
+  const int live = plan_pick<kCtas>(c.pages, 0, s, [&](int i) { return c.refs[i] > 0; },
                                 [](int, int) {});
   // as many pages in use lie behind the first `live` as there are holes among them
-  const int moves = cluster_pick(c.pages, c.pages, s,
+  const int moves = plan_pick<kCtas>(c.pages, c.pages, s,
                                  [&](int i) { return i >= live && c.refs[i] > 0; },
                                  [&](int k, int i) { p.from[k] = i; });
-  cluster_pick(c.pages, c.pages, s, [&](int i) { return i < live && c.refs[i] <= 0; },
+  plan_pick<kCtas>(c.pages, c.pages, s, [&](int i) { return i < live && c.refs[i] <= 0; },
                [&](int k, int i) { p.to[k] = i; });
-  for (int i = t; i < c.pages; i += kPlanAll) p.map[i] = i;
-  cl.sync();
-  for (int k = t; k < moves; k += kPlanAll) {
+  for (int i = t; i < c.pages; i += P::kAll) p.map[i] = i;
+  P::sync();
+  for (int k = t; k < moves; k += P::kAll) {
     const int a = __ldcg(p.from + k), b = __ldcg(p.to + k);
     p.map[a] = b;
     c.refs[b] = c.refs[a];
@@ -485,6 +520,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 }
 
 __global__ void __launch_bounds__(256) compact_kernel(CacheView c, PlanWs p) {
+  chain_wait();
   const int count = *p.count;
   if (count == 0) return;
   const long long all = (long long)gridDim.x * blockDim.x;
@@ -519,6 +555,29 @@ cudaError_t done() {
   return cudaGetLastError();
 }
 
+// Launches a plan over `work` pages. One block passes its barriers faster, eight read
+// more at a time: an extend takes 6.0 and 8.6 us over 1,000 pages, 9.0 and 9.3 over 8,000, 16
+// and 11 over 32,000. Freeing goes over table entries, with an atomic and a store each:
+// 5.4 and 3.3 us for 4,096 of them, so they count four times.
+template <class... A, class... B>
+cudaError_t launch_plan(long long work, cudaStream_t st, void (*one)(A...), void (*eight)(A...),
+                        B... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 8;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  const bool large = work > 8192;
+  cfg.gridDim = dim3(large ? 8 : 1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = large ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, large ? eight : one, static_cast<A>(args)...);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
 }  // namespace
 
 size_t cache_workspace_bytes(int pages, int slots, int n) {
@@ -528,9 +587,8 @@ size_t cache_workspace_bytes(int pages, int slots, int n) {
 
 cudaError_t cache_extend(const CacheView& c, const int* seqs, int n, const int* cu, int tokens,
                          int* pos, void* ws, cudaStream_t st) {
-  extend_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, seqs, n, cu, tokens, pos,
-                                                    plan_ws(ws, c.pages, c.slots, n));
-  return done();
+  return launch_plan(c.pages, st, extend_kernel<1>, extend_kernel<8>, c, seqs, n, cu, tokens, pos,
+                     plan_ws(ws, c.pages, c.slots, n));
 }
 
 cudaError_t cache_write(const CacheView& c, int layer, const void* K, const void* V,
@@ -547,34 +605,36 @@ cudaError_t cache_write(const CacheView& c, int layer, const void* K, const void
 cudaError_t cache_fork(const CacheView& c, const int* src, const int* dst, int n, void* ws,
                        cudaStream_t st) {
   const PlanWs p = plan_ws(ws, c.pages, c.slots, n);
-  fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, src, dst, n, p);
-  if (cudaError_t e = done()) return e;
+  if (cudaError_t e = launch_plan(c.pages, st, fork_plan_kernel<1>, fork_plan_kernel<8>, c, src,
+                                  dst, n, p))
+    return e;
   const long long entries = (long long)n * c.width, copies = copy_threads(c, n);
-  fork_kernel<<<data_blocks(entries > copies ? entries : copies), 256, 0, st>>>(c, src, dst, n, p);
-  return done();
+  return launch_chained(fork_kernel, data_blocks(entries > copies ? entries : copies), 256, 0, st,
+                        true, c, src, dst, n, p);
 }
 
 cudaError_t cache_free(const CacheView& c, const int* seqs, int n, void* ws, cudaStream_t st) {
-  free_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, seqs, n, plan_ws(ws, c.pages, c.slots, n));
-  return done();
+  return launch_plan(4ll * n * c.width, st, free_kernel<1>, free_kernel<8>, c, seqs, n,
+                     plan_ws(ws, c.pages, c.slots, n));
 }
 
 cudaError_t cache_copy(const CacheView& c, const int* src, const int* dst, int n, void* ws,
                        cudaStream_t st) {
   const PlanWs p = plan_ws(ws, c.pages, c.slots, n);
-  copy_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, src, dst, n, p);
-  if (cudaError_t e = done()) return e;
-  copy_kernel<<<data_blocks(copy_threads(c, n)), 256, 0, st>>>(c, p, src, dst, n);
-  return done();
+  if (cudaError_t e = launch_plan(n, st, copy_plan_kernel<1>, copy_plan_kernel<8>, c, src, dst, n,
+                                  p))
+    return e;
+  return launch_chained(copy_kernel, data_blocks(copy_threads(c, n)), 256, 0, st, true, c, p, src,
+                        dst, n);
 }
 
 cudaError_t cache_compact(const CacheView& c, void* ws, cudaStream_t st) {
   const PlanWs p = plan_ws(ws, c.pages, c.slots, 0);
-  compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(c, p);
-  if (cudaError_t e = done()) return e;
+  if (cudaError_t e = launch_plan(c.pages, st, compact_plan_kernel<1>, compact_plan_kernel<8>, c, p))
+    return e;
   const long long entries = (long long)c.slots * c.width, copies = copy_threads(c, c.pages);
-  compact_kernel<<<data_blocks(entries > copies ? entries : copies), 256, 0, st>>>(c, p);
-  return done();
+  return launch_chained(compact_kernel, data_blocks(entries > copies ? entries : copies), 256, 0,
+                        st, true, c, p);
 }
 
 }  // namespace fa
