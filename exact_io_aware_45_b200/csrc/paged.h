@@ -50,11 +50,12 @@ struct Phase {
   int n = 0;           // streams
   int items = 0;
   int fold = 1;        // partial results per piece and row
-  bool blocked = false;  // partial O lies as [128-row block][32 columns][row][32], with the
-                         // 16-byte chunk c of a row's 32 columns at c ^ (row & 7)
+  bool blocked = false;  // partial O lies as [128-row block][d / 4][row][4]
   int over = 4;        // units of an item beside its tiles
   int snap = 2;        // tiles that a cut keeps from an item's ends
   int least = 4;       // units that a stream is worth
+  int yield = 0;       // shared phase: units of the own phase that take an SM as long as one
+                       // of its own, where the own phase runs beside it
   float* o = nullptr;  // partial results: [items + n][fold][rows][d], normalised
   float* lse = nullptr;  // [items + n][fold][rows], base 2
 };
@@ -78,8 +79,8 @@ struct PagedArgs {
 // Launches a kernel of a call's chain (shared phase, own phase, join). With `after`
 // it may start before the kernel ahead of it in the stream has finished, once that
 // has let it (chain_next); it then has to wait (chain_wait) before it reads that
-// kernel's results, or before it ends if it reads none: the end of the chain's last
-// kernel implies the end of all.
+// kernel's results, or, if it reads none, let one block wait before it ends (chain_end): the end
+// of the chain's last kernel implies the end of all, and the other blocks make room.
 template <class... P, class... A>
 cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
                            cudaStream_t st, bool after, A... args) {
@@ -103,6 +104,9 @@ __device__ __forceinline__ void chain_next() {
 }
 __device__ __forceinline__ void chain_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void chain_end() {
+  if (blockIdx.x == 0) chain_wait();
 }
 #endif
 

@@ -64,10 +64,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 // 16 bytes global -> shared; `bytes` of them are read, the rest become zero.
-__device__ __forceinline__ void copy16(uint32_t dst, const char* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(bytes)
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(
+                   dst),
+               "l"(src), "r"(bytes), "l"(policy)
                : "memory");
+}
+// K and V that one row tile reads leave L2 first: the partial results are to stay there.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+  uint64_t p;
+  if (once) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 __device__ __forceinline__ void copy_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
   chain_next();
   sched::Walk w;
   if (!sched::begin(a, pre, stream, w)) {
-    chain_wait();
+    chain_end();
     return;
   }
 
@@ -131,6 +139,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
   const float cap2 = a.softcap * kLog2e;
   const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
   const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
+  const uint64_t policy = l2_policy(ph.rt == 1);
 
   while (w.x < w.end) {
     const sched::Piece pc = sched::next(a, pre, w);
@@ -158,8 +167,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
                                (((c & 7) ^ (row & 7)) << 4);
           // rows that no query sees are not read and count as zero
           const int bytes = edge && (j + row < pc.lo || j + row >= pc.hi) ? 0 : 16;
-          copy16(dst, k + i * 512, bytes);
-          copy16(dst + kStageBytes / 2, v + i * 512, bytes);
+          copy16(dst, k + i * 512, bytes, policy);
+          copy16(dst + kStageBytes / 2, v + i * 512, bytes, policy);
         }
       }
     };
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
     }
   }
   copy_wait<0>();
-  chain_wait();
+  chain_end();
 }
 
 template <int D, int NT>

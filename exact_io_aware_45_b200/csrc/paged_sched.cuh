@@ -65,8 +65,11 @@ __device__ __forceinline__ void pre_keys(const PagedArgs& a, int least, int most
 // W units in n even ranges: the first `extra` are one longer.
 struct Cuts {
   int W, n, each, extra;
-  __device__ Cuts(const Phase& ph, int units) : W(units) {
+  // `beside`: units of the own phase, when this is the shared one
+  __device__ Cuts(const Phase& ph, int units, int beside = 0) : W(units) {
     n = max(1, min(ph.n, W / ph.least));
+    // leaves the own phase, which runs beside it, the SMs that let both end together
+    if (ph.yield) n = max(1, min(n, (int)((long long)ph.n * W / (W + beside / ph.yield))));
     each = W / n;
     extra = W - each * n;
   }
@@ -179,7 +182,7 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
   if (pre) {
     pre_keys(a, t.least, t.most, w.lo, w.hi);
     w.u = units_of(a.pre, w.lo, w.hi);
-    const Cuts c(a.pre, a.pre.items * w.u);
+    const Cuts c(a.pre, a.pre.items * w.u, t.W);
     if (i >= c.n) return false;
     const int x0 = c.at(i), x1 = c.at(i + 1);
     w.item = x0 / w.u;
@@ -298,6 +301,12 @@ __device__ __forceinline__ Row row_at(const PagedArgs& a, bool pre, int h, int b
   if (a.wl >= 0) o.lo = max((long long)o.lo, (long long)pos - a.wl);
   o.out = (b * a.Hq + h * a.G) * a.T + q;
   return o;
+}
+// Index of row r of a piece in LSE (and, times d, in Q and O).
+__device__ __forceinline__ int out_of(const PagedArgs& a, bool pre, const Piece& p, int r) {
+  int b = p.b, q = p.row0 + r;
+  if (pre) b = q / a.TG, q -= b * a.TG;
+  return (b * a.Hq + p.h * a.G) * a.T + q;
 }
 // Row r of a piece.
 __device__ __forceinline__ Row row_of(const PagedArgs& a, bool pre, const Piece& p, int r) {

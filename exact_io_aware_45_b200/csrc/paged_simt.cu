@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
   chain_next();
   sched::Walk w;
   if (!sched::begin(a, pre, blockIdx.x, w)) {         // the block's warps walk alike
-    chain_wait();
+    chain_end();
     return;
   }
   const T* Q = static_cast<const T*>(a.Q);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, co
       }
     }
   }
-  chain_wait();
+  chain_end();
 }
 
 template <typename T, int D>
@@ -245,16 +245,17 @@ cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
 // issues two shuffles, a load and d / 32 multiply-adds.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinMaxRows = 16;
+constexpr int kChunk = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a, const int rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArgs a, const int rows) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
   struct RowPieces {
     int own, own_head, own_next;   // partial results of the own phase, first slots
     int all, pre_head, pre_next;   // of both phases
     int own_row, pre_row;
   };
-  __shared__ float part_o[kJoinWarps][D], part_sum[kJoinWarps];
+  __shared__ float part_o[kJoinWarps][D], part_sum[kJoinWarps], part_top[kJoinWarps];
   __shared__ RowPieces info[kJoinMaxRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y, in_b = a.c.Hkv * a.TG;
@@ -282,8 +283,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
         const int pr = b * a.TG + q, prt = pr / a.pre.rows;
         p.pre_head = h * a.pre.rt + prt;
         p.pre_row = pr - prt * a.pre.rows;
-        sched::pieces_of(a.pre, p.pre_head * pu, pu, sched::Cuts(a.pre, a.pre.items * pu), first,
-                         more);
+        sched::pieces_of(a.pre, p.pre_head * pu, pu, sched::Cuts(a.pre, a.pre.items * pu, t.W),
+                         first, more);
         p.pre_next = a.pre.items + first;
         p.all += (more + 1) * a.pre.fold;
       } else if (more == 0 && a.own.fold == 1) {
@@ -293,11 +294,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
     }
   }
   __syncthreads();
-  chain_wait();                                         // the partial results are there
   // `ways` warps a row
   int ways = kJoinWarps;
   while (ways > 1 && ways * count > kJoinWarps) ways >>= 1;
   const int way = warp & (ways - 1);
+  bool waited = false;
   // shared rows are done in one go, all warps meeting below
   const int stop = ways > 1 ? kJoinWarps / ways : count;
   for (int i = warp / ways; i < stop; i += kJoinWarps / ways) {
@@ -314,63 +315,68 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
       const int slot = k ? (own ? p.own_next : p.pre_next) + k : (own ? p.own_head : p.pre_head);
       return (slot * ph.fold + f) * ph.rows + (own ? p.own_row : p.pre_row);
     };
-    float top = -INFINITY, lse = -INFINITY;             // lane k: of partial result k
-    int at = 0;
-    for (int k = lane; k < p.all; k += 32) {
-      at = at_of(k);
-      lse = (k < p.own ? a.own.lse : a.pre.lse)[at];
-      top = fmaxf(top, lse);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[kPer];
+    float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int k0 = 0; k0 < p.all; k0 += 32) {
-      if (p.all > 32) {
-        lse = -INFINITY;
-        if (k0 + lane < p.all) {
-          at = at_of(k0 + lane);
-          lse = (k0 + lane < p.own ? a.own.lse : a.pre.lse)[at];
-        }
-      }
-      const float weight = exp2f(lse - ref);
-      const int n = min(32, p.all - k0), own = p.own - k0;
-#pragma unroll 4
-      for (int k = way; k < n; k += ways) {
-        const float c = __shfl_sync(~0u, weight, k);
+    // kChunk partial results at a time: their O and LSE are on their way together
+    for (int k0 = way * kChunk; k0 < p.all; k0 += ways * kChunk) {
+      const int n = min(kChunk, p.all - k0), own = p.own - k0;
+      const int at = lane < n ? at_of(k0 + lane) : 0;   // lane k: of partial result k0 + k
+      if (!waited) chain_wait();                        // the partial results are there
+      waited = true;
+      float lse = -INFINITY;
+      if (lane < n) lse = (lane < own ? a.own.lse : a.pre.lse)[at];
+      float v[kChunk][kPer];
+      const int col = lane * kPer;
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
         const int row = __shfl_sync(~0u, at, k);
         const Phase& ph = k < own ? a.own : a.pre;
-        const int col = lane * kPer;
         const float* from = ph.o + (size_t)row * D + col;
         if (ph.blocked)
-          from = ph.o + (size_t)(row >> 7) * (128 * D) + (col >> 5) * (128 * 32) +
-                 (row & 127) * 32 + ((((col >> 2) & 7) ^ (row & 7)) << 2) + (col & 3);
-        sum += c;
-        if (col < D) {
-          float v[kPer];
-          load_f<kPer>(from, v);
+          from = ph.o + (size_t)(row >> 7) * (128 * D) + (col >> 2) * (128 * 4) +
+                 (row & 127) * 4 + (col & 3);
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
-        }
+        for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
+        if (k < n && col < D) load_f<kPer>(from, v[k]);
+      }
+      float m = lse;
+#pragma unroll
+      for (int o = kChunk / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      m = fmaxf(__shfl_sync(~0u, m, 0), top);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float old = exp2f(top - ref), weight = exp2f(lse - ref);
+      top = m;
+      sum *= old;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] *= old;
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        const float c = __shfl_sync(~0u, weight, k);    // 0 for k >= n
+        sum += c;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[k][e], acc[e]);
       }
     }
     if (ways > 1) {
       if (lane * kPer < D)
 #pragma unroll
         for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
-      if (lane == 0) part_sum[warp] = sum;
+      if (lane == 0) part_top[warp] = top, part_sum[warp] = sum;
       __syncthreads();
-      if (way) return;
+      if (way) break;
+      for (int k = 0; k < ways; ++k) top = fmaxf(top, part_top[warp + k]);
+      const float ref = top == -INFINITY ? 0.f : top;
       sum = 0.f;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
       for (int k = 0; k < ways; ++k) {
-        sum += part_sum[warp + k];
+        const float c = exp2f(part_top[warp + k] - ref);
+        sum = fmaf(c, part_sum[warp + k], sum);
         if (lane * kPer < D)
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) acc[e] += part_o[warp + k][lane * kPer + e];
+          for (int e = 0; e < kPer; ++e)
+            acc[e] = fmaf(c, part_o[warp + k][lane * kPer + e], acc[e]);
       }
     }
     if (p.all == 0) continue;
@@ -383,14 +389,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedArgs a
         store_f(static_cast<T*>(a.O) + out * D + lane * kPer + e, acc[e] * inv);
     if (lane == 0) a.LSE[out] = (top + log2f(sum)) * 0.6931471805599453f;
   }
+  if (!waited) chain_wait();                            // this kernel's end implies the others'
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, cudaStream_t st) {
-  // enough blocks for the device first, then rows that share a block's set-up
+  // as many blocks as are resident at once (four an SM), then rows that share a block's set-up
   const long long all = (long long)a.B * a.c.Hkv * a.TG;
   int rows = 1;
-  while (rows < kJoinMaxRows && all / (2 * rows) >= 300) rows *= 2;
+  while (rows < kJoinMaxRows && all > 592 * rows) rows *= 2;
   const dim3 grid((a.c.Hkv * a.TG + rows - 1) / rows, a.B);
   return launch_chained(join_kernel<T, D>, grid, kJoinWarps * 32, 0, st, true, a, rows);
 }

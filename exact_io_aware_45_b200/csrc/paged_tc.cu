@@ -45,14 +45,12 @@ constexpr int kMaxSlots = 8;
 // kTwo: two query tiles.
 template <int D, bool kTwo>
 struct Cfg {
-  static constexpr int kSlots = D == 64 ? 8 : (kTwo ? 4 : 5);
+  static constexpr int kSlots = D == 64 ? 8 : (kTwo ? 5 : 6);
   static constexpr int kTileBytes = kN * D * 2;      // one K or V tile
   static constexpr int kQBytes = kM * D * 2;
   static constexpr int kBlock = 128 * 128;           // one 64-column block
-  static constexpr int kStage = 128 * 128;           // 32 fp32 columns of 128 rows
   static constexpr int kOffKV = (kTwo ? 2 : 1) * kQBytes;
-  static constexpr int kOffStage = kOffKV + kSlots * kTileBytes;
-  static constexpr int kBytes = kOffStage + 2 * kStage + 1024;
+  static constexpr int kBytes = kOffKV + kSlots * kTileBytes + 1024;
   static constexpr uint32_t kS = 128;                // TMEM columns: S_t at 128 t,
   static constexpr uint32_t kO = 256;                // O_t at 256 + D t,
   static constexpr uint32_t kP = 64;                 // P_t in the upper half of S_t
@@ -89,12 +87,6 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// 16-byte aligned shared -> global bulk store.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-               "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -113,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   chain_next();
   sched::Walk w;
   if (!sched::begin(a, pre, blockIdx.x, w)) {            // the same answer in every warp
-    chain_wait();
+    chain_end();
     return;
   }
   if (threadIdx.x == 0) {
@@ -145,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (s.skip) {                                          // nothing is in flight yet
     __syncthreads();
     if (warp == 2) tmem_dealloc(tm, 512);
-    chain_wait();
+    chain_end();
     return;
   }
   const Guard guard{&s.abort, a.c.err};
@@ -166,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) s.walk[warp - 4] = v;
     __syncwarp();
     row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
-    if (item_row < pc.rows) row = sched::row_of(a, pre, pc, item_row);
+    if (item_row < pc.rows) row.out = sched::out_of(a, pre, pc, item_row);
     // this warp's rows of Q (or half of them) into the swizzled tile, whole rows at a time
     constexpr int kVecs = D / 8, kRows = 32 / kVecs, kMine = kTwo ? 32 : 16;
     constexpr int kLoads = kMine / kRows;
@@ -181,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[i] = __ldg(reinterpret_cast<const int4*>(static_cast<const __nv_bfloat16*>(a.Q) +
                                                    (size_t)out * D) + c);
     }
+    if (item_row < pc.rows) row = sched::row_of(a, pre, pc, item_row);   // Q is on its way
     uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + (c >> 3) * C::kBlock;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -377,8 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = xform ? 1.f : scale2;
     const float cap2 = a.softcap * kLog2e;
     const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
-    uint8_t* const stage = base + C::kOffStage + t * C::kStage;
-    const int tid = threadIdx.x - 128 - t * 128;
     uint32_t cnt = 0;                                    // this warpgroup's tiles so far
     if (lane == 0) s.walk[warp - 4] = w;
     __syncwarp();
@@ -485,9 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (slot < 0) a.LSE[row.out] = lse2 * kLn2;
         else ph.lse[at + r] = lse2;
       }
-      const int rows = min(kM, kTwo ? pc.rows - t * kM : pc.rows);
-      // of the tile's row 0 (own phase: the rows of a sequence and KV head are contiguous)
-      const int out0 = (pc.b * a.Hq + pc.h * a.G) * a.T + pc.row0 + t * kM;
+      const int out = row.out;
+      const bool real = item_row < pc.rows;
       // the next piece's Q goes in before this one's result goes out, so that its first
       // scores are computed meanwhile
       const bool more = s.walk[warp - 4].x < s.walk[warp - 4].end;
@@ -495,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch();
         have_q();
       }
-      // Rows through shared memory, 32 columns at a time: partial results as they lie there
-      // (the join knows the swizzle), 16 KB by one bulk store; results in whole lines.
+      // Partial results go out with a row in each lane, [16-byte chunk][row], so that a
+      // warp writes 512 contiguous bytes straight from its registers.
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         uint32_t o[32];
@@ -506,40 +496,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (slot >= 0 && k > 0) {
-          if (tid == 0) bulk_wait_read0();
-          named_sync(1 + t, 128);
-        }
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(stage + r * 128 + ((q ^ (r & 7)) << 4)) =
-              make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                          __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         if (slot >= 0) {
-          fence_async_smem();
-          named_sync(1 + t, 128);
-          if (tid == 0) {
-            bulk_store(ph.o + at * D + k * (kM * 32), stage, C::kStage);
-            bulk_commit();
-          }
-        } else {
-          named_sync(1 + t, 128);
+          float4* to = reinterpret_cast<float4*>(ph.o + at * D) + k * 8 * kM + r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = i * 16 + (tid >> 3), q = tid & 7;
-            const float4 v =
-                *reinterpret_cast<const float4*>(stage + rr * 128 + ((q ^ (rr & 7)) << 4));
-            if (rr < rows)
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) +
-                                        (size_t)(out0 + rr) * D + k * 32 + q * 4) =
-                  make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          for (int q = 0; q < 8; ++q)
+            to[q * kM] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                     __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+        } else if (real) {
+          uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) +
+                                               (size_t)out * D + k * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* x = &o[8 * q];
+            to[q] = make_uint4(
+                pack_bf16(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                pack_bf16(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                pack_bf16(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                pack_bf16(__uint_as_float(x[6]), __uint_as_float(x[7])));
           }
-          named_sync(1 + t, 128);
         }
-      }
-      if (slot >= 0) {
-        if (tid == 0) bulk_wait_read0();
-        named_sync(1 + t, 128);
       }
       tc_fence_before();
       if (!more) break;
@@ -551,8 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tm, 512);
   }
-  if (threadIdx.x == 128 || threadIdx.x == 256) bulk_wait0();   // its partial results are written
-  chain_wait();
+  chain_end();
 }
 
 template <int D, bool kTwo>
