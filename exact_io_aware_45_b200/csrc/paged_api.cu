@@ -121,9 +121,12 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
       p.rows = p.fold == 2 ? kTcRows : 2 * kTcRows;
       p.tile_log2 = kTcTileLog2;
       p.n = sms;
-      p.over = 3;          // a further piece costs a stream 6 us, a tile 2 us
+      // A piece costs a stream about 10 us beside its tiles of 2 us each; still, short
+      // prefixes are cut down to single tiles: 512 tokens behind 128 sequences of 8 heads took
+      // 98 us in one stream per head, 31 us in one per tile.
+      p.over = 5;
       p.snap = 1;
-      p.least = 5;
+      p.least = 1;
       break;
   }
   p.rt = (rows + p.rows - 1) / p.rows;
