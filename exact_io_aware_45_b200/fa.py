@@ -125,7 +125,7 @@ def lib() -> ctypes.CDLL:
         L.fa_debug_set_stall.restype = _I
         L.fa_bwd_varlen_workspace_size.argtypes = [_I, _I, _I, _I, _I]
         L.fa_bwd_varlen_workspace_size.restype = _S
-        C = ctypes.POINTER(FaCache)
+        C = _P          # const fa_cache*: an address, or byref() of one
         for n, args in (("fa_cache_extend", [C, _P, _I, _P, _I, _P, _P, _S, _P]),
                         ("fa_cache_write", [C, _I, _P, _P, _P, _P, _I, _P, _I, _P]),
                         ("fa_cache_fork", [C, _P, _P, _I, _P, _S, _P]),
@@ -551,12 +551,16 @@ class PagedCache:
         self._c = FaCache(_ptr(k), _ptr(v), k.stride(0), k.stride(1), L, P, Hkv, ps, d,
                           _dtype_code(k.dtype), _ptr(table), _ptr(lens), _ptr(refs),
                           table.shape[0], table.shape[1], _ptr(self.err))
-        self._ref = ctypes.byref(self._c)
         # a call costs the host as much as small ones cost the GPU: what every call needs is
         # looked up once (workspace sizes by the sizes they depend on)
-        self._torch, self._lib, self._index = torch, lib(), k.device.index
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
-        self._sizes = {}
+        self._torch, self._index = torch, k.device.index
+        self._ref = ctypes.addressof(self._c)
+        self._current, self._raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self._int32, self._sizes = torch.int32, {}
+        L = lib()
+        self._extend, self._write, self._free = L.fa_cache_extend, L.fa_cache_write, L.fa_cache_free
+        self._fork, self._copy, self._compact = L.fa_cache_fork, L.fa_cache_copy, L.fa_cache_compact
+        self._paged, self._shared = L.fa_fwd_paged, L.fa_fwd_shared
         if fa_cache_workspace_size(self._ref, 0) == 0:
             raise ValueError("unsupported cache: page_size is 16, 32, 64 or 128, d 16, 32, 64 or "
                              "128, strides are multiples of 16 bytes")
@@ -575,25 +579,21 @@ class PagedCache:
 
     def _list(self, t) -> int:
         """The length of a list of slots, pages, positions or offsets."""
-        if t.dtype is not self._torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+        if t.dtype is not self._int32 or t.dim() != 1 or not t.is_contiguous() or \
                 t.get_device() != self._index:
             raise ValueError("a list is a contiguous int32 tensor on the cache's device")
         return t.numel()
 
-    def _call(self, name, *args):
+    def _call(self, fn, *args):
         """A library call on the cache's device and its current stream."""
-        cuda = self._torch.cuda
-        fn = getattr(self._lib, name)
-        if cuda.current_device() == self._index:
-            s = fn(self._ref, *args, self._raw_stream(self._index))
+        index = self._index
+        if self._current() == index:
+            s = fn(self._ref, *args, self._raw_stream(index))
         else:
-            with cuda.device(self._index):
-                s = fn(self._ref, *args, self._raw_stream(self._index))
-        if s != FA_OK:
-            raise FaError(s, name)
-
-    def _empty(self, size, dtype):
-        return self._torch.empty(size, dtype=dtype, device=self.device)
+            with self._torch.cuda.device(index):
+                s = fn(self._ref, *args, self._raw_stream(index))
+        if s:
+            raise FaError(s, fn.__name__)
 
     def _workspace(self, *key):
         """A new workspace: for lists of (n,) entries, or attention of (B, T, Hq, shared)."""
@@ -602,7 +602,7 @@ class PagedCache:
             fn = fa_cache_workspace_size if len(key) == 1 else fa_paged_workspace_size
             with self._torch.cuda.device(self._index):
                 size = self._sizes[key] = fn(self._ref, *key)
-        return self._empty(size, self._torch.uint8), size
+        return self.err.new_empty(size, dtype=self._torch.uint8), size
 
     def extend(self, seqs, tokens):
         """Makes room for new tokens: `tokens` of each sequence, or cu_seqlens
@@ -613,9 +613,9 @@ class PagedCache:
             if self._list(tokens) != n + 1:
                 raise ValueError("cu_seqlens has one entry more than the list of sequences")
             cu, each = tokens.data_ptr(), 0
-        pos = self._empty(n, self._torch.int32)
+        pos = seqs.new_empty(n)
         ws, size = self._workspace(n)
-        self._call("fa_cache_extend", seqs.data_ptr(), n, cu, each, pos.data_ptr(),
+        self._call(self._extend, seqs.data_ptr(), n, cu, each, pos.data_ptr(),
                    ws.data_ptr(), size)
         return pos
 
@@ -637,34 +637,34 @@ class PagedCache:
                 raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
         if len(shape) != 3 or shape[1] != self.Hkv or shape[2] != self.d:
             raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
-        self._call("fa_cache_write", layer, k.data_ptr(), v.data_ptr(), seqs.data_ptr(),
+        self._call(self._write, layer, k.data_ptr(), v.data_ptr(), seqs.data_ptr(),
                    pos.data_ptr(), n, cu, shape[0])
 
-    def _pairs(self, name, src, dst):
+    def _pairs(self, fn, src, dst):
         n = self._list(src)
         if self._list(dst) != n:
             raise ValueError("lists of different lengths")
         ws, size = self._workspace(n)
-        self._call(name, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), size)
+        self._call(fn, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), size)
 
     def fork(self, src, dst):
         """Makes the empty sequences dst copies of src: full pages are shared."""
-        self._pairs("fa_cache_fork", src, dst)
+        self._pairs(self._fork, src, dst)
 
     def copy_pages(self, src, dst):
         """Copies pages src to pages dst in all layers."""
-        self._pairs("fa_cache_copy", src, dst)
+        self._pairs(self._copy, src, dst)
 
     def free(self, seqs):
         """Empties sequences and gives up their pages."""
         n = self._list(seqs)
         ws, size = self._workspace(n)
-        self._call("fa_cache_free", seqs.data_ptr(), n, ws.data_ptr(), size)
+        self._call(self._free, seqs.data_ptr(), n, ws.data_ptr(), size)
 
     def compact(self):
         """Moves the pages in use to the front of the pool."""
         ws, size = self._workspace(0)
-        self._call("fa_cache_compact", ws.data_ptr(), size)
+        self._call(self._compact, ws.data_ptr(), size)
 
     def check(self):
         """Raises FaError if the device refused a call since the last check
@@ -690,7 +690,7 @@ def _forward_cache(q, cache, layer, shared, seqs, scale, causal, window_left, so
             not out.is_contiguous():
         raise ValueError("out is like q")
     if lse is None:
-        lse = cache._empty((B, Hq, T), torch.float32)
+        lse = q.new_empty((B, Hq, T), dtype=torch.float32)
     elif lse.shape != shape[:3] or lse.dtype != torch.float32 or lse.get_device() != index or \
             not lse.is_contiguous():
         raise ValueError("lse is float32 [B, Hq, T]")
@@ -705,10 +705,10 @@ def _forward_cache(q, cache, layer, shared, seqs, scale, causal, window_left, so
     slots = 0 if seqs is None else seqs.data_ptr()
     causal = 1 if causal else 0
     if shared:
-        cache._call("fa_fwd_shared", layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), slots, B,
+        cache._call(cache._shared, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), slots, B,
                     T, Hq, shared, scale, causal, window_left, softcap, workspace.data_ptr(), size)
     else:
-        cache._call("fa_fwd_paged", layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), slots, B, T,
+        cache._call(cache._paged, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), slots, B, T,
                     Hq, scale, causal, window_left, softcap, workspace.data_ptr(), size)
     return out, lse
 
