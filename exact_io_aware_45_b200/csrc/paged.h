@@ -49,15 +49,14 @@ struct Phase {
   int rt = 0;          // row tiles per (sequence, KV head); per KV head in the shared phase
   int n = 0;           // streams
   int items = 0;
-  int fold = 1;        // partial results per piece and row
   bool blocked = false;  // partial O lies as [128-row block][d / 4][row][4]
   int over = 4;        // units of an item beside its tiles
   int snap = 2;        // tiles that a cut keeps from an item's ends
   int least = 4;       // units that a stream is worth
   int yield = 0;       // shared phase: units of the own phase that take an SM as long as one
                        // of its own, where the own phase runs beside it
-  float* o = nullptr;  // partial results: [items + n][fold][rows][d], normalised
-  float* lse = nullptr;  // [items + n][fold][rows], base 2
+  float* o = nullptr;  // partial results: [items + n][rows][d], normalised
+  float* lse = nullptr;  // [items + n][rows], base 2
 };
 
 struct PagedArgs {
@@ -115,10 +114,10 @@ cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st)
 constexpr int kSimtRows = 8, kSimtTileLog2 = 5, kSimtBlocksPerSm = 4;
 // mma.sync kernel for few packed rows (bf16, d in {64, 128}); a stream is a warp.
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
-constexpr int kMmaMaxRows = 16, kMmaWarps = 4, kMmaBlocksPerSm = 2;
+constexpr int kMmaRows = 16, kMmaWarps = 4, kMmaBlocksPerSm = 2;
 constexpr int mma_tile_log2(int d) { return d == 128 ? 4 : 5; }
 // tcgen05 kernel for many packed rows (bf16, d in {64, 128}); a stream is a CTA.
-// fold = 2: one query tile of 128 rows, its key tiles dealt to two warpgroups.
+// Items of 128 rows (one query tile, its key tiles dealt to two warpgroups) or 256.
 cudaError_t paged_tc(const PagedArgs& a, bool pre, cudaStream_t st);
 constexpr int kTcTileLog2 = 7, kTcRows = 128;
 // Joins the partial results of both phases.

@@ -88,13 +88,15 @@ int sm_count() {
 }
 
 // Kernels of a phase: bf16 with d of 64 or 128 runs on the tensor cores, all else
-// on the CUDA cores. Up to kMmaMaxRows packed rows the mma.sync kernel reads K
-// and V at full bandwidth; above, it would read them once per kMmaMaxRows rows, and
-// the tcgen05 kernel takes 128 or 256 rows at once.
+// on the CUDA cores. The mma.sync kernel reads K and V once per kMmaRows packed rows and
+// is quick with short sequences; the tcgen05 kernel takes 128 or 256 rows at once, which
+// costs an item more to begin and end. At 24 to 32 rows (two row tiles) 64 sequences of 20
+// to 300 tokens take 27 and 42 us, 32 of 100 to 2,000 38 and 45, 8 of 8,192 89 and 68;
+// at 40 the first is at 34, 51 and 122 us, and the second ahead from some hundred tokens on.
 enum Family { kSimt, kMma, kTc };
 Family family(const CacheView& v, int rows) {
   if (v.row_bytes != 2 * v.d || v.d < 64) return kSimt;
-  return rows <= kMmaMaxRows ? kMma : kTc;
+  return rows <= 2 * kMmaRows ? kMma : kTc;
 }
 
 // The work division of a phase of `groups` sequences and KV heads with `rows`
@@ -110,15 +112,14 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
       p.n = sms * kSimtBlocksPerSm;
       break;
     case kMma:
-      p.rows = rows <= 8 ? 8 : kMmaMaxRows;
+      p.rows = rows <= 8 ? 8 : kMmaRows;
       p.tile_log2 = mma_tile_log2(v.d);
       per = kMmaWarps;
       p.n = sms * kMmaWarps * kMmaBlocksPerSm;
       break;
     case kTc:
-      p.fold = rows <= kTcRows ? 2 : 1;
+      p.rows = rows <= kTcRows ? kTcRows : 2 * kTcRows;
       p.blocked = true;
-      p.rows = p.fold == 2 ? kTcRows : 2 * kTcRows;
       p.tile_log2 = kTcTileLog2;
       p.n = sms;
       // A piece costs a stream about 10 us beside its tiles of 2 us each; still, short
@@ -155,16 +156,16 @@ bool plan(PagedArgs& a, int sms) {
   // run side by side on different SMs. A tile of 256 rows takes an SM 2.2 us, 8 KB of an own
   // stream 0.11 us (an SM by itself gets about one and a half times its share of the bandwidth).
   if (a.shared && family(a.c, a.B * a.TG) == kTc && family(a.c, a.TG) == kMma)
-    a.pre.yield = a.pre.fold == 2 ? 10 : 20;
+    a.pre.yield = a.pre.rows == kTcRows ? 10 : 20;
   const long long most = keys / 16 + 8;
   for (const Phase* p : {&a.own, &a.pre})
-    if (((long long)p->items + p->n) * p->rows * p->fold >= (1ll << 31)) return false;
+    if (((long long)p->items + p->n) * p->rows >= (1ll << 31)) return false;
   return a.own.items * most < (1ll << 31) - (1 << 20) &&
          a.pre.items * most < (1ll << 31) - (1 << 20);
 }
 
 size_t phase_bytes(const Phase& p, int d, size_t* lse_at) {
-  const size_t rows = (size_t)(p.items + p.n) * p.rows * p.fold;
+  const size_t rows = (size_t)(p.items + p.n) * p.rows;
   *lse_at = align256(rows * d * 4);
   return *lse_at + align256(rows * 4);
 }

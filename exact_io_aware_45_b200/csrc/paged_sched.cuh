@@ -9,7 +9,7 @@
 // `over` units or closer than `snap` tiles to either end moves to that end, which
 // spares partial results of a few tiles; n shrinks to W / `least` for little work.
 //
-// An item that one stream covers whole and that nothing else adds to is written
+// An item that one stream covers whole and that no other phase adds to is written
 // to O and LSE directly. Otherwise each of its pieces goes to a slot of its
 // own: the piece with the item's first tile to slot `item`, a piece that begins
 // with stream i's first tile to slot items + i.
@@ -270,7 +270,7 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, Walk& w) {
   const int base = w.lo >> ph.tile_log2;
   p.t0 = base + max(0, from - ph.over);
   p.t1 = base + to - ph.over;
-  const bool alone = from == 0 && to == w.u && a.shared == 0 && ph.fold == 1;
+  const bool alone = from == 0 && to == w.u && a.shared == 0;
   p.slot = alone ? -1 : (from == 0 ? w.item : ph.items + w.stream);
   w.x = w.s + to;
   if (w.x < w.end) {

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArg
       int first, more;
       sched::pieces_of(a.own, t.before + in * u, u, cuts, first, more);
       RowPieces p;
-      p.own = (more + 1) * a.own.fold;
+      p.own = more + 1;
       p.own_head = b * a.c.Hkv * a.own.rt + in;
       p.own_next = a.own.items + first;
       p.own_row = q - rt * a.own.rows;
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArg
         sched::pieces_of(a.pre, p.pre_head * pu, pu, sched::Cuts(a.pre, a.pre.items * pu, t.W),
                          first, more);
         p.pre_next = a.pre.items + first;
-        p.all += (more + 1) * a.pre.fold;
-      } else if (more == 0 && a.own.fold == 1) {
+        p.all += more + 1;
+      } else if (more == 0) {
         p.all = 0;                                      // written by its only piece
       }
       info[lane] = p;
@@ -310,10 +310,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArg
       const bool own = k < p.own;
       const Phase& ph = own ? a.own : a.pre;
       if (!own) k -= p.own;
-      const int f = ph.fold == 2 ? k & 1 : 0;
-      k >>= ph.fold == 2 ? 1 : 0;
       const int slot = k ? (own ? p.own_next : p.pre_next) + k : (own ? p.own_head : p.pre_head);
-      return (slot * ph.fold + f) * ph.rows + (own ? p.own_row : p.pre_row);
+      return slot * ph.rows + (own ? p.own_row : p.pre_row);
     };
     float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll

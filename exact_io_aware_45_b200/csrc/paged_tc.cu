@@ -9,7 +9,8 @@
 //  * two query tiles (more than 128 packed rows): warpgroup t has rows
 //    128 t .. 128 t + 127 of the item, and every K/V tile serves both;
 //  * one query tile: the warpgroups take the item's key tiles alternately, with running
-//    statistics and an accumulator each, and leave two partial results to the join.
+//    statistics and an accumulator each. At the end each reads half the columns of both
+//    accumulators (a row is the same TMEM lane in both) and joins them.
 //
 // K and V pages are copied by three loader warps with cp.async (any page size;
 // a TMA box ends with its page, and at 16 tokens a page the boxes of one 128-key tile cost
@@ -45,12 +46,13 @@ constexpr int kMaxSlots = 8;
 // kTwo: two query tiles.
 template <int D, bool kTwo>
 struct Cfg {
-  static constexpr int kSlots = D == 64 ? 8 : (kTwo ? 5 : 6);
+  static constexpr int kSlots = D == 64 ? 8 : 5;
   static constexpr int kTileBytes = kN * D * 2;      // one K or V tile
   static constexpr int kQBytes = kM * D * 2;
   static constexpr int kBlock = 128 * 128;           // one 64-column block
   static constexpr int kOffKV = (kTwo ? 2 : 1) * kQBytes;
-  static constexpr int kBytes = kOffKV + kSlots * kTileBytes + 1024;
+  static constexpr int kOffStat = kOffKV + kSlots * kTileBytes;
+  static constexpr int kBytes = kOffStat + (kTwo ? 0 : 2 * kM * 8) + 1024;
   static constexpr uint32_t kS = 128;                // TMEM columns: S_t at 128 t,
   static constexpr uint32_t kO = 256;                // O_t at 256 + D t,
   static constexpr uint32_t kP = 64;                 // P_t in the upper half of S_t
@@ -145,13 +147,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     return mbar_wait_ready_first(bar, parity, guard);
   };
 
-  // Softmax warps: row `r` of query tile t (of the one query tile), and the next piece's
-  // rows and Q.
+  // Softmax warps: row `r` of query tile t (of the one query tile).
   const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
   const int item_row = kTwo ? t * kM + r : r;
   sched::Piece pc;
   sched::Row row;
-  auto fetch = [&] {
+  // Q of a piece: this warp's rows of it (half of them, when two warpgroups share a tile),
+  // whole rows at a time, first into registers ...
+  constexpr int kQVecs = D / 8, kQRows = 32 / kQVecs, kQLoads = (kTwo ? 32 : 16) / kQRows;
+  const int q_chunk = lane % kQVecs, q_row = (kTwo ? 0 : t * 16) + lane / kQVecs;
+  auto next_piece = [&](int4 (&x)[kQLoads]) {
     sched::Walk v = s.walk[warp - 4];
     pc = sched::next(a, pre, v);
     __syncwarp();
@@ -159,28 +164,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     row.lo = 0, row.hi = 0x7fffffff, row.out = 0;
     if (item_row < pc.rows) row.out = sched::out_of(a, pre, pc, item_row);
-    // this warp's rows of Q (or half of them) into the swizzled tile, whole rows at a time
-    constexpr int kVecs = D / 8, kRows = 32 / kVecs, kMine = kTwo ? 32 : 16;
-    constexpr int kLoads = kMine / kRows;
-    const int c = lane % kVecs, r0 = (kTwo ? 0 : t * 16) + lane / kVecs;
-    const int w0 = (warp & 3) * 32, top = kTwo ? t * kM : 0;
-    int4 x[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int rr = r0 + i * kRows, out = __shfl_sync(~0u, row.out, rr);
+    for (int i = 0; i < kQLoads; ++i) {
+      const int rr = q_row + i * kQRows, out = __shfl_sync(~0u, row.out, rr);
       x[i] = make_int4(0, 0, 0, 0);
-      if (top + w0 + rr < pc.rows)
+      if ((kTwo ? t * kM : 0) + (warp & 3) * 32 + rr < pc.rows)
         x[i] = __ldg(reinterpret_cast<const int4*>(static_cast<const __nv_bfloat16*>(a.Q) +
-                                                   (size_t)out * D) + c);
+                                                   (size_t)out * D) + q_chunk);
     }
     if (item_row < pc.rows) row = sched::row_of(a, pre, pc, item_row);   // Q is on its way
-    uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + (c >> 3) * C::kBlock;
+  };
+  // ... and, once nothing reads the last piece's any more, into the swizzled tile.
+  auto give_q = [&](const int4 (&x)[kQLoads]) {
+    uint8_t* to = base + (kTwo ? t * C::kQBytes : 0) + (q_chunk >> 3) * C::kBlock;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int rr = w0 + r0 + i * kRows;
-      *reinterpret_cast<int4*>(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+    for (int i = 0; i < kQLoads; ++i) {
+      const int rr = (warp & 3) * 32 + q_row + i * kQRows;
+      *reinterpret_cast<int4*>(to + rr * 128 + (((q_chunk & 7) ^ (rr & 7)) << 4)) = x[i];
     }
     fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_full[kTwo ? t : 0]);
   };
 
   if (warp == 0 || warp == 2 || warp == 3) {
@@ -373,12 +377,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cnt = 0;                                    // this warpgroup's tiles so far
     if (lane == 0) s.walk[warp - 4] = w;
     __syncwarp();
-    fetch();
-    auto have_q = [&] {                                  // what fetch() stored may be read
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.q_full[kTwo ? t : 0]);
-    };
-    have_q();
+    {
+      int4 q[kQLoads];
+      next_piece(q);
+      give_q(q);
+    }
     for (uint32_t np = 0;; ++np) {
       const int lo_all = __reduce_max_sync(~0u, row.lo), hi_all = __reduce_min_sync(~0u, row.hi);
       float m_ref = -INFINITY, l = 0.f;
@@ -462,61 +465,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = false;
         ++cnt;
       }
-      // every S and P V of the piece has completed: its accumulators may be read,
-      // its Q buffers overwritten
+      // The piece is done but for its result. The next one's Q goes in before the result goes
+      // out, so that its first scores are not waited for (and with one query tile, whose
+      // pieces are short, it is fetched before the last P V has completed).
+      const int slot = pc.slot, out = row.out;
+      const bool real = item_row < pc.rows, both = pc.t1 - pc.t0 > 1;
+      const bool more = s.walk[warp - 4].x < s.walk[warp - 4].end;
+      int4 q[kQLoads];
+      if (!kTwo && more) next_piece(q);
+      // every S and P V has completed: the accumulators may be read, the Q buffers overwritten
       bool got = wait(&s.o_ready[t], np & 1);
       if (!kTwo) got = wait(&s.o_ready[t ^ 1], np & 1) && got;
-      const bool some = __all_sync(~0u, got) && !first;
+      got = __all_sync(~0u, got);
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      const float lse2 = m_ref + log2f(l);
-      const int slot = pc.slot;
-      const long long at = (long long)slot * (ph.rows * ph.fold) + t * kM;   // partial row 0
-      if (item_row < pc.rows) {
-        if (slot < 0) a.LSE[row.out] = lse2 * kLn2;
-        else ph.lse[at + r] = lse2;
+      if (kTwo && more) next_piece(q);
+      if (more) give_q(q);
+      // this thread's factors for the accumulators of warpgroups 0 and 1 (kTwo: its own)
+      float f0, f1 = 0.f, lse2;
+      if constexpr (kTwo) {
+        f0 = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        lse2 = m_ref + log2f(l);
+      } else {
+        float2* const stat = reinterpret_cast<float2*>(base + C::kOffStat);   // (m, l) of both
+        stat[t * kM + r] = make_float2(m_ref, l);
+        named_sync(1, 256);
+        const float2 a0 = stat[r], a1 = stat[kM + r];
+        const float top = fmaxf(a0.x, a1.x), ref = top == -INFINITY ? 0.f : top;
+        f0 = ex2(a0.x - ref), f1 = ex2(a1.x - ref);
+        const float sum = f0 * a0.y + f1 * a1.y;
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        f0 *= inv, f1 *= inv;
+        lse2 = top + log2f(sum);
       }
-      const int out = row.out;
-      const bool real = item_row < pc.rows;
-      // the next piece's Q goes in before this one's result goes out, so that its first
-      // scores are computed meanwhile
-      const bool more = s.walk[warp - 4].x < s.walk[warp - 4].end;
-      if (more) {
-        fetch();
-        have_q();
+      const long long at = (long long)slot * ph.rows + (kTwo ? t * kM : 0);   // partial row 0
+      if (real && (kTwo || t == 0)) {
+        if (slot < 0) a.LSE[out] = lse2 * kLn2;
+        else ph.lse[at + r] = lse2;
       }
       // Partial results go out with a row in each lane, [16-byte chunk][row], so that a
       // warp writes 512 contiguous bytes straight from its registers.
+      constexpr int kChunks = kTwo ? D / 32 : D / 64;    // 32 columns each
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
+      for (int i = 0; i < kChunks; ++i) {
+        const int k = kTwo ? i : t * kChunks + i;
         uint32_t o[32];
-        if (some) {
-          tmem_ld32(o_reg + k * 32, o);
-        } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+        if (got) {
+          tmem_ld32((kTwo ? o_reg : tm + C::kO + lanes) + k * 32, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          if (!kTwo && both) {
+            uint32_t o1[32];
+            tmem_ld32(tm + C::kO + D + lanes + k * 32, o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         if (slot >= 0) {
           float4* to = reinterpret_cast<float4*>(ph.o + at * D) + k * 8 * kM + r;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            to[q * kM] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                     __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+          for (int c4 = 0; c4 < 8; ++c4)
+            to[c4 * kM] =
+                make_float4(__uint_as_float(o[4 * c4]), __uint_as_float(o[4 * c4 + 1]),
+                            __uint_as_float(o[4 * c4 + 2]), __uint_as_float(o[4 * c4 + 3]));
         } else if (real) {
           uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) +
                                                (size_t)out * D + k * 32);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* x = &o[8 * q];
-            to[q] = make_uint4(
-                pack_bf16(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                pack_bf16(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                pack_bf16(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                pack_bf16(__uint_as_float(x[6]), __uint_as_float(x[7])));
+          for (int c8 = 0; c8 < 4; ++c8) {
+            const uint32_t* v = &o[8 * c8];
+            to[c8] = make_uint4(
+                pack_bf16(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                pack_bf16(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                pack_bf16(__uint_as_float(v[4]), __uint_as_float(v[5])),
+                pack_bf16(__uint_as_float(v[6]), __uint_as_float(v[7])));
           }
         }
+      }
+      // both warpgroups have read both accumulators before the next piece's P V
+      if (!kTwo) {
+        tc_fence_before();
+        named_sync(1, 256);
       }
       tc_fence_before();
       if (!more) break;
@@ -545,7 +576,7 @@ cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
 }  // namespace
 
 cudaError_t paged_tc(const PagedArgs& a, bool pre, cudaStream_t st) {
-  const bool two = (pre ? a.pre : a.own).fold == 1;
+  const bool two = (pre ? a.pre : a.own).rows > kM;
   if (a.c.d == 128) return two ? launch<128, true>(a, pre, st) : launch<128, false>(a, pre, st);
   return two ? launch<64, true>(a, pre, st) : launch<64, false>(a, pre, st);
 }
