@@ -55,6 +55,7 @@ struct Phase {
   int least = 4;       // units that a stream is worth
   int yield = 0;       // shared phase: units of the own phase that take an SM as long as one
                        // of its own, where the own phase runs beside it
+  int sms = 0;         // SMs of the device
   float* o = nullptr;  // partial results: [items + n][rows][d], normalised
   float* lse = nullptr;  // [items + n][rows], base 2
 };

@@ -104,6 +104,7 @@ Family family(const CacheView& v, int rows) {
 // workspace query and the call agree.
 Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) {
   Phase p;
+  p.sms = sms;
   int per = 1;           // streams of a block
   switch (family(v, rows)) {
     case kSimt:

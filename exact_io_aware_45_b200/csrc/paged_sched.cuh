@@ -69,7 +69,7 @@ struct Cuts {
   __device__ Cuts(const Phase& ph, int units, int beside = 0) : W(units) {
     n = max(1, min(ph.n, W / ph.least));
     // leaves the own phase, which runs beside it, the SMs that let both end together
-    if (ph.yield) n = max(1, min(n, (int)((long long)ph.n * W / (W + beside / ph.yield))));
+    if (ph.yield) n = max(1, min(n, (int)((long long)ph.sms * W / (W + beside / ph.yield))));
     each = W / n;
     extra = W - each * n;
   }

@@ -320,6 +320,28 @@ def test_paged_long_sequences_are_cut_and_joined(dtype, d, lens, Hq, Hkv, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,Hq,Hkv", [(17, 4, 2), (40, 4, 2), (64, 2, 1), (129, 2, 2), (200, 4, 2)])
+@pytest.mark.parametrize("wl,causal,cap,scale", [(-1, True, 0.0, None), (50, True, 0.0, None),
+                                                 (300, False, 8.0, None), (-1, False, 0.0, -0.1),
+                                                 (-1, True, 0.0, 0.0)])
+def test_paged_chunks_of_tokens(d, T, Hq, Hkv, wl, causal, cap, scale):
+    """Many rows per KV head, one and two query tiles of them and more."""
+    attend_case([0, 1, T - 3, T, 260, 700], Hq, Hkv, d, 16, "bf16", T=T, wl=wl, causal=causal,
+                cap=cap, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,T", [(3, 9), (12, 3), (40, 4)])
+@pytest.mark.parametrize("wl,causal,cap,scale", [(100, True, 0.0, None), (-1, False, 8.0, None),
+                                                 (40, True, 5.0, -0.2), (-1, True, 0.0, 0.0)])
+def test_shared_rows_in_one_and_two_tiles(d, B, T, wl, causal, cap, scale):
+    attend_case([128 + (31 * b) % 200 for b in range(B)], 8, 2, d, 64, "bf16", T=T, shared=128,
+                wl=wl, causal=causal, cap=cap, scale=scale)
+
+
+@pytest.mark.gpu
 def test_paged_many_sequences():
     """More sequences than threads of a block that scans their lengths."""
     rng = np.random.default_rng(3)
