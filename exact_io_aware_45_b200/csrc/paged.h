@@ -49,7 +49,7 @@ struct Phase {
   int rt = 0;          // row tiles per (sequence, KV head); per KV head in the shared phase
   int n = 0;           // streams
   int items = 0;
-  bool blocked = false;  // partial O lies as [128-row block][d / 4][row][4]
+  bool blocked = false;  // partial O lies as [128-row block][d / 8][row][8]
   int over = 4;        // units of an item beside its tiles
   int snap = 2;        // tiles that a cut keeps from an item's ends
   int least = 4;       // units that a stream is worth

@@ -155,9 +155,9 @@ bool plan(PagedArgs& a, int sms) {
   a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, a.shared, sms) : Phase();
   // The tcgen05 kernel leaves the memory idle and the mma.sync kernel the tensor cores: they
   // run side by side on different SMs. A tile of 256 rows takes an SM 2.2 us, 8 KB of an own
-  // stream 0.11 us (an SM by itself gets about one and a half times its share of the bandwidth).
+  // stream 0.14 us.
   if (a.shared && family(a.c, a.B * a.TG) == kTc && family(a.c, a.TG) == kMma)
-    a.pre.yield = a.pre.rows == kTcRows ? 10 : 20;
+    a.pre.yield = a.pre.rows == kTcRows ? 8 : 16;
   const long long most = keys / 16 + 8;
   for (const Phase* p : {&a.own, &a.pre})
     if (((long long)p->items + p->n) * p->rows >= (1ll << 31)) return false;

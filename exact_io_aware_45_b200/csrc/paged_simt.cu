@@ -245,7 +245,7 @@ cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
 // issues two shuffles, a load and d / 32 multiply-adds.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinMaxRows = 16;
-constexpr int kChunk = 8;
+constexpr int kChunk = 8;              // at most 16; 10 spilled and took 1 us more
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArgs a, const int rows) {
@@ -332,15 +332,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArg
         const Phase& ph = k < own ? a.own : a.pre;
         const float* from = ph.o + (size_t)row * D + col;
         if (ph.blocked)
-          from = ph.o + (size_t)(row >> 7) * (128 * D) + (col >> 2) * (128 * 4) +
-                 (row & 127) * 4 + (col & 3);
+          from = ph.o + (size_t)(row >> 7) * (128 * D) + (col >> 3) * (128 * 8) +
+                 (row & 127) * 8 + (col & 7);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
         if (k < n && col < D) load_f<kPer>(from, v[k]);
       }
       float m = lse;
 #pragma unroll
-      for (int o = kChunk / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
       m = fmaxf(__shfl_sync(~0u, m, 0), top);
       const float ref = m == -INFINITY ? 0.f : m;
       const float old = exp2f(top - ref), weight = exp2f(lse - ref);

@@ -89,6 +89,12 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// 32 bytes of registers to global memory.
+__device__ __forceinline__ void store32(float* to, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
 __device__ __forceinline__ void copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -502,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (slot < 0) a.LSE[out] = lse2 * kLn2;
         else ph.lse[at + r] = lse2;
       }
-      // Partial results go out with a row in each lane, [16-byte chunk][row], so that a
-      // warp writes 512 contiguous bytes straight from its registers.
+      // Partial results go out with a row in each lane, [32-byte chunk][row], so that a
+      // warp writes 1 KB at once straight from its registers, and the join reads whole sectors.
       constexpr int kChunks = kTwo ? D / 32 : D / 64;    // 32 columns each
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
@@ -524,12 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (slot >= 0) {
-          float4* to = reinterpret_cast<float4*>(ph.o + at * D) + k * 8 * kM + r;
+          float* to = ph.o + at * D + (k * 4 * kM + r) * 8;
 #pragma unroll
-          for (int c4 = 0; c4 < 8; ++c4)
-            to[c4 * kM] =
-                make_float4(__uint_as_float(o[4 * c4]), __uint_as_float(o[4 * c4 + 1]),
-                            __uint_as_float(o[4 * c4 + 2]), __uint_as_float(o[4 * c4 + 3]));
+          for (int c8 = 0; c8 < 4; ++c8) store32(to + c8 * kM * 8, &o[8 * c8]);
         } else if (real) {
           uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) +
                                                (size_t)out * D + k * 32);
