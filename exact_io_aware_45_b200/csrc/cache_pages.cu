@@ -258,9 +258,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // One warp per token: its position follows from the list (a chain of five dependent
 // loads, for which its data does not wait), then 16-byte pieces of its Hkv heads go to the
-// heads' rows of the page. 76 MB of tokens take 28 us
-// (5.4 TB/s read and written), the 48 tokens of a decoding step 3.4 us (3.7 with the loads
-// behind the chain).
+// heads' rows of the page. 76 MB of tokens take 28 us (5.4 TB/s read and written), the 48
+// tokens of a decoding step 3.4 us (3.7 with the data's loads behind the chain).
 __global__ void __launch_bounds__(256)
     write_kernel(CacheView c, char* lk, char* lv, const char* K, const char* V, const int* seqs,
                  const int* pos, int n, const int* cu, int total) {

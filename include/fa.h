@@ -425,8 +425,8 @@ fa_status fa_cache_extend(const fa_cache* cache, const int* seqs, int n, const i
  * aligned) into one layer: token j of sequence i, row cu_seqlens[i] + j (row
  * i * (total / n) + j without cu_seqlens), goes to position pos[i] + j. Rows of
  * a sequence with pos < 0 are skipped. A position behind the sequence's length, or in a page
- * that more than one table holds, is not written and reported as FA_ERR_CACHE.
- * No workspace.
+ * that more than one table holds, is not written and reported as FA_ERR_CACHE. A
+ * position that the call names twice gets either row. No workspace.
  */
 fa_status fa_cache_write(const fa_cache* cache, int layer, const void* K, const void* V,
                          const int* seqs, const int* pos, int n, const int* cu_seqlens,
@@ -468,9 +468,10 @@ fa_status fa_cache_compact(const fa_cache* cache, void* workspace, size_t worksp
  *   (causal == 0 or j <= i) and (window_left < 0 or j >= i - window_left);
  * softcap > 0 caps the scores as in fa_mods. A query that sees no key (an
  * empty slot, i < 0, seqs[b] out of range) gets O = 0 and LSE = -inf. K and V
- * rows that no query of the call sees may hold anything. A non-finite V row
- * may spread to every query of a call that sees a key in the 128-key
- * neighbourhood. Table entries out of range read page 0.
+ * rows that no query of the call sees may hold anything. A non-finite V row that
+ * one query sees may spread to the call's other queries of that KV head. Table
+ * entries out of range read page 0, and a length past the table is cut to it, so
+ * inconsistent state gives wrong results but no access outside the cache.
  * workspace: fa_paged_workspace_size bytes, device, 16-byte aligned, no
  * initial value; one call at a time. A bounded wait that runs out is reported
  * through cache->err (FA_ERR_TIMEOUT). Deterministic.
