@@ -72,35 +72,35 @@ PlanWs plan_ws(void* ws, int pages, int slots, int n) {
 }
 
 struct PlanShared {
-  int warp[kPlanThreads / 32];
-  int total;
+  long long warp[kPlanThreads / 32];
   int mine;      // this CTA's count, read by the others through the cluster
 };
 
 // Exclusive prefix sum of v over the block; `total` is the block's sum.
-__device__ int block_scan(int v, PlanShared& s, int& total) {
+template <class T>
+__device__ T block_scan(T v, PlanShared& s, T& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, x, o);
+    const T y = __shfl_up_sync(~0u, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) s.warp[w] = x;
   __syncthreads();
   if (w == 0) {
-    int y = lane < kPlanThreads / 32 ? s.warp[lane] : 0;
+    T y = lane < kPlanThreads / 32 ? (T)s.warp[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int z = __shfl_up_sync(~0u, y, o);
+    for (int o = 1; o < kPlanThreads / 32; o <<= 1) {
+      const T z = __shfl_up_sync(~0u, y, o);
       if (lane >= o) y += z;
     }
     if (lane < kPlanThreads / 32) s.warp[lane] = y;
   }
   __syncthreads();
-  total = s.warp[kPlanThreads / 32 - 1];
-  return x - v + (w ? s.warp[w - 1] : 0);
+  total = (T)s.warp[kPlanThreads / 32 - 1];
+  return x - v + (w ? (T)s.warp[w - 1] : 0);
 }
 
 // Zeroes the header and the bits; everyone sees them afterwards.
@@ -174,15 +174,15 @@ __device__ int plan_pick(int n, int limit, PlanShared& s, Pred pred, Emit emit) 
 template <class P, class Need>
 __device__ void list_scan(int n, int* at, PlanShared& s, Need need) {
   if (P::rank() == 0) {
-    int base = 0;
+    long long base = 0;                         // needs of a bad list may add up to anything
     for (int b = 0; b < n; b += kPlanThreads) {
       const int i = b + threadIdx.x;
-      int total;
-      const int x = block_scan(i < n ? need(i) : 0, s, total);
-      if (i < n) at[i] = min(base + x, 1 << 30);
-      base = min(base + total, 1 << 30);
+      long long total;
+      const long long x = block_scan<long long>(i < n ? need(i) : 0, s, total);
+      if (i < n) at[i] = (int)min(base + x, 1ll << 30);
+      base = min(base + total, 1ll << 30);
     }
-    if (threadIdx.x == 0) at[n] = base;
+    if (threadIdx.x == 0) at[n] = (int)base;
   }
 }
 
@@ -543,11 +543,7 @@ __global__ void __launch_bounds__(256) compact_kernel(CacheView c, PlanWs p) {
 
 // Enough blocks of 256 threads to fill the device, fewer for little work.
 int data_blocks(long long threads) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  long long b = (threads + 255) / 256;
-  const long long most = (long long)sms * 8;
+  const long long b = (threads + 255) / 256, most = 8ll * sm_count();
   return (int)(b < 1 ? 1 : (b > most ? most : b));
 }
 

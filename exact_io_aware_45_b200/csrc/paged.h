@@ -27,6 +27,9 @@ struct CacheView {
   unsigned* err;
 };
 
+// SMs of the current device, asked for once per device.
+int sm_count();
+
 cudaError_t cache_extend(const CacheView& c, const int* seqs, int n, const int* cu, int tokens,
                          int* pos, void* ws, cudaStream_t st);
 cudaError_t cache_write(const CacheView& c, int layer, const void* K, const void* V,

@@ -9,6 +9,18 @@
 #include "paged.h"
 
 namespace fa {
+
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -73,18 +85,6 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
   if (!ws || !aligned(ws, 16) || bytes < cache_workspace_bytes(v.pages, v.slots, n))
     return FA_ERR_INVALID_ARG;
   return FA_OK;
-}
-
-// SMs of the current device, asked for once per device.
-int sm_count() {
-  static std::atomic<int> known[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  return n;
 }
 
 // Kernels of a phase: bf16 with d of 64 or 128 runs on the tensor cores, all else

@@ -608,11 +608,12 @@ class PagedCache:
         """Makes room for new tokens: `tokens` of each sequence, or cu_seqlens
         (int32 [n + 1]). Returns the positions of the first ones, int32 [n]."""
         n = self._list(seqs)
-        cu, each = 0, tokens       # (a list stays referenced until its use is enqueued)
-        if not isinstance(tokens, int):
+        if isinstance(tokens, self._torch.Tensor):     # (referenced until its use is enqueued)
             if self._list(tokens) != n + 1:
                 raise ValueError("cu_seqlens has one entry more than the list of sequences")
             cu, each = tokens.data_ptr(), 0
+        else:
+            cu, each = 0, int(tokens)
         pos = seqs.new_empty(n)
         ws, size = self._workspace(n)
         self._call(self._extend, seqs.data_ptr(), n, cu, each, pos.data_ptr(),
@@ -716,8 +717,8 @@ def _forward_cache(q, cache, layer, shared, seqs, scale, causal, window_left, so
 def forward_paged(q, cache: PagedCache, layer: int, seqs=None, scale: Optional[float] = None,
                   causal: bool = True, window_left: int = -1, softcap: float = 0.0, out=None,
                   lse=None, workspace=None):
-    """O, LSE of the last T tokens of each sequence over the cache (fa_fwd_paged).
-    q [B, Hq, T, d]; seqs int32 [B], or None for slots 0 .. B-1. A workspace
+    """O, LSE of the last T tokens of each sequence over the cache (fa_fwd_paged;
+    without gradients). q [B, Hq, T, d]; seqs int32 [B], or None for slots 0 .. B-1. A workspace
     (fa_paged_workspace_size bytes) serves one call at a time."""
     return _forward_cache(q, cache, layer, 0, seqs, scale, causal, window_left, softcap, out, lse,
                           workspace)

@@ -487,7 +487,7 @@ def same_state(cache, pool):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("pages,seqs,dtype", [(40, 12, "f32"), (700, 30, "bf16"),
-                                              (5000, 600, "bf16")])
+                                              (5000, 600, "bf16"), (20000, 300, "bf16")])
 def test_pages_follow_the_oracle(pages, seqs, dtype):
     """A long run of operations; K and V stay with their tokens."""
     import torch
@@ -610,6 +610,61 @@ def test_copy_pages(page, Hkv, d, dtype, layout):
     cache.check()
     k[:, dst], v[:, dst] = k[:, src], v[:, src]
     assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
+
+
+@pytest.mark.gpu
+def test_copy_of_many_pages_and_its_refusal():
+    import torch
+    cache = fa.PagedCache.new(1, 20000, 1, 16, 16, 2, 2)
+    cache.k.normal_(), cache.v.normal_()
+    k = cache.k.clone()
+    order = np.random.default_rng(0).permutation(20000)
+    src, dst = order[:9500], order[9500:19000]
+    cache.copy_pages(ints(src), ints(dst))
+    cache.check()
+    k[:, torch.from_numpy(dst).cuda()] = k[:, torch.from_numpy(src).cuda()]
+    assert torch.equal(cache.k, k)
+    dst[-1] = src[0]
+    cache.copy_pages(ints(src[::-1].copy()), ints(dst))
+    with pytest.raises(fa.FaError):
+        cache.check()
+    assert torch.equal(cache.k, k)
+
+
+@pytest.mark.gpu
+def test_extension_by_more_than_there_is():
+    """Needs that add up past 32 bits are refused like others."""
+    n = 900
+    cache = fa.PagedCache.new(1, 20, 1, 128, 16, n, 2000000)
+    cache.extend(ints(np.arange(n)), 250_000_000)
+    with pytest.raises(fa.FaError):
+        cache.check()
+    assert not cache.lens.any() and not cache.refs.any()
+
+
+@pytest.mark.gpu
+def test_calls_on_a_side_stream():
+    """A whole step on a stream of its own, its inputs made there; nothing waits for another."""
+    import torch
+    res = []
+    for side in (False, True):
+        s = torch.cuda.Stream() if side else torch.cuda.current_stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            g = torch.Generator(device="cuda").manual_seed(1)
+            cache = fa.PagedCache.new(1, 300, 2, 16, 64, 40, 40)
+            slots = ints(np.arange(30))
+            for n in (100, 1, 1):
+                pos = cache.extend(slots, n)
+                k, v = (torch.randn(30 * n, 2, 64, generator=g, device="cuda").bfloat16()
+                        for _ in range(2))
+                cache.write(0, k, v, slots, pos)
+            q = torch.randn(30, 8, 1, 64, generator=g, device="cuda").bfloat16()
+            r = fa.forward_paged(q, cache, 0, slots)
+            cache.check()
+        res.append([x.clone() for x in r])
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
 # ------------------------------------------------------------------ together (GPU)
