@@ -117,7 +117,6 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
       p.tile_log2 = mma_tile_log2(v.d);
       per = kMmaWarps;
       p.n = sms * kMmaWarps * kMmaBlocksPerSm;
-      p.over = 3;          // 71 us for the drafted tokens, 75 with 4; the others the same
       break;
     case kTc:
       p.rows = rows <= kTcRows ? kTcRows : 2 * kTcRows;
