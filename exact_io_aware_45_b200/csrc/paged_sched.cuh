@@ -69,7 +69,10 @@ struct Cuts {
   __device__ Cuts(const Phase& ph, int units, int beside = 0) : W(units) {
     n = max(1, min(ph.n, W / ph.least));
     // leaves the own phase, which runs beside it, the SMs that let both end together
-    if (ph.yield) n = max(1, min(n, (int)((long long)ph.sms * W / (W + beside / ph.yield))));
+    if (ph.yield) {
+      const long long all = (long long)W + beside / ph.yield;
+      n = max(1, min(n, (int)((long long)ph.sms * W / all)));
+    }
     each = W / n;
     extra = W - each * n;
   }
@@ -103,10 +106,12 @@ __device__ __forceinline__ void pieces_of(const Phase& ph, int s, int u, const C
 // `b`, the smallest and the largest length, and that of b. All lanes call it.
 struct Batch {
   int W, before, least, most, len;
+  int lead;          // the first sequence that reaches farthest into the shared prefix
   int lane_len;      // of sequence `lane`
 };
 __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
-  Batch t{0, 0, 0x7fffffff, 0, 0, 0};
+  Batch t{0, 0, 0x7fffffff, 0, 0, 0, 0};
+  int reach = -1;
   const int per_b = a.c.Hkv * a.own.rt, lane = threadIdx.x & 31;
   constexpr int kAtOnce = 4;                      // dependent loads in flight per lane
   for (int i0 = lane; i0 < a.B; i0 += 32 * kAtOnce) {
@@ -125,6 +130,8 @@ __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
       if (i < b) t.before += u;
       if (i == b) t.len = len[k];
       t.least = min(t.least, len[k]);
+      const int into = min(len[k], a.shared);
+      if (into > reach) reach = into, t.lead = i;
       t.most = max(t.most, len[k]);
     }
   }
@@ -132,6 +139,7 @@ __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
   t.before = __reduce_add_sync(~0u, t.before);
   t.least = __reduce_min_sync(~0u, t.least);
   t.most = __reduce_max_sync(~0u, t.most);
+  t.lead = __reduce_min_sync(~0u, reach == __reduce_max_sync(~0u, reach) ? t.lead : 0x7fffffff);
   t.len = __reduce_max_sync(~0u, t.len);
   return t;
 }
@@ -144,7 +152,7 @@ struct Walk {
   int item;          // (b * Hkv + h) * rt + row tile; (h * rt + row tile) in the shared phase
   int b, h, r;       // sequence (own phase), KV head, row tile
   int lo, hi;        // keys of the item
-  int slot, len;     // of sequence b; the first sequence's slot in the shared phase
+  int slot, len;     // of sequence b; the leading sequence's slot in the shared phase
   int slot1, len1;   // of the next sequence, and the slot after it: loaded ahead, since a
   int slot2;         // chain of loads per sequence would stall short ones
 };
@@ -194,7 +202,8 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
     w.h = w.item / a.pre.rt;
     w.r = w.item - w.h * a.pre.rt;
     w.b = w.len = 0;
-    w.slot = slot_of(a, 0);
+    w.slot = slot_of(a, t.lead);   // its table names all of the prefix that is in sight (the
+                                   // first sequence may be padding, or shorter)
     return true;
   }
   const Cuts c(a.own, t.W);
@@ -247,7 +256,7 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
 struct Piece {
   int h;             // KV head
   int b, len;        // sequence and its length (own phase)
-  int table;         // slot whose table names the keys (the first sequence's in the shared phase)
+  int table;         // slot whose table names the keys (the leading one's in the shared phase)
   int row0, rows;    // rows: (g, t) of sequence b, or (b, g, t) in the shared phase
   int lo, hi;        // keys in sight of any row
   int t0, t1;        // key tiles [t0, t1), counted from key 0

@@ -484,10 +484,11 @@ fa_status fa_fwd_paged(const fa_cache* cache, int layer, const void* Q, void* O,
 /*
  * fa_fwd_paged for sequences that begin with the same `shared` tokens (a
  * multiple of page_size; e.g. forks of one prompt): their keys and values are
- * read through the table of the FIRST sequence, once for the whole batch, and
- * each sequence's own table from token `shared` on. Results are those of
- * fa_fwd_paged when the tables agree up to there. A sequence shorter than
- * `shared` sees its length of them.
+ * read through ONE table, that of the first sequence which reaches farthest into
+ * them, once for the whole batch, and each sequence's own table from token `shared`
+ * on. Results are those of fa_fwd_paged when the tables agree up to there, as far
+ * as a sequence reaches. A sequence shorter than `shared` sees its length of them;
+ * padding (an empty slot, seqs[b] out of range) may stand anywhere in the batch.
  */
 fa_status fa_fwd_shared(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
                         const int* seqs, int B, int T, int Hq, int shared, float scale,

@@ -214,8 +214,11 @@ def build(lens, Hkv, d, page, dtype, layers=1, layout="plain", shared=0, seed=0,
     table = np.full((slots, width), -1, dtype=np.int32)
     length = np.zeros(slots, dtype=np.int32)
     first, at = shared // page, shared // page
-    # only the first sequence's table names the shared pages
-    table[slot[0], :first] = order[:first]
+    # only the first sequence that reaches farthest into the shared pages names them
+    reach = [min(n, shared) for n in lens]
+    lead = reach.index(max(reach))
+    held = -(-reach[lead] // page)
+    table[slot[lead], :held] = order[:held]
     g = torch.Generator(device="cuda").manual_seed(seed)
     head = [torch.randn(layers, Hkv, shared, d, generator=g, device="cuda").to(dt)
             for _ in range(2)]
@@ -231,7 +234,7 @@ def build(lens, Hkv, d, page, dtype, layers=1, layout="plain", shared=0, seed=0,
             for j, p in enumerate(mine):
                 part = y[:, :, j * page:(j + 1) * page]
                 x[:, int(p), :, :part.shape[2]] = part
-            if b == 0:
+            if b == lead:
                 top = max(lens)         # what no sequence is long enough to see stays NaN
                 for j in range(first):
                     m = max(0, min(page, top - j * page))
@@ -391,6 +394,26 @@ def test_shared_prefix_longer_than_every_sequence(dtype, d):
     """What no sequence is long enough to see of it holds NaN."""
     attend_case([90, 0, 17, 3], 8, 2, d, 32, dtype, T=2, shared=256)
     attend_case([0, 0], 8, 2, d, 32, dtype, shared=64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,reps", [("bf16", 128, 1), ("bf16", 64, 9), ("f32", 64, 2)])
+def test_shared_padding_stands_anywhere(dtype, d, reps):
+    """Slots out of range and an empty one before, between and behind the sequences."""
+    import torch
+    lens = [0, 40, 300, 256, 511] * reps
+    cache, seqs, dense = build(lens, 2, d, 32, dtype, shared=256)
+    order = [-1, 0, 1, None, 2, 3, None, 4]             # None: out of range; -1 as well
+    order = [o if o is None or o < 0 else o + 5 * i for i in range(reps) for o in order]
+    slots = torch.tensor([-1 if o == -1 else 10 ** 6 if o is None else int(seqs[o])
+                          for o in order], dtype=torch.int32, device="cuda")
+    real = [i for i, o in enumerate(order) if o is not None and o >= 0]
+    q = torch.randn(len(order), 8, 3, d, device="cuda").to(cache.dtype)
+    o, lse = fa.forward_shared(q, cache, 0, 256, slots)
+    cache.check()
+    check(o[real], lse[real], q[real], dense, lens, 0, dtype, d ** -0.5)
+    pad = [i for i in range(len(order)) if i not in real]
+    assert not o[pad].any() and torch.isneginf(lse[pad]).all()
 
 
 @pytest.mark.gpu
