@@ -117,7 +117,7 @@ struct Pages {
 // NT: n-tiles of eight packed query rows.
 template <int D, int NT>
 __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
-    mma_kernel(const PagedArgs a, const bool pre) {
+    mma_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
   constexpr int kTile = 1 << mma_tile_log2(D), kGroups = kTile / 16;   // 16 keys a group
   constexpr int kGroupBytes = 16 * D * 2;
   constexpr int kRowVecs = D / 8;                            // 16-byte chunks of a row
@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
   const Phase& ph = pre ? a.pre : a.own;
   // neighbouring streams on different SMs: little work is spread over all of them
   const int stream = warp * gridDim.x + blockIdx.x;
+  warm_args(a);
   chain_next();
   sched::Walk w;
   if (!sched::begin(a, pre, stream, w)) {

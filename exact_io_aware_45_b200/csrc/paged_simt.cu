@@ -71,12 +71,13 @@ struct SimtShared {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) simt_kernel(const PagedArgs a, const bool pre) {
+__global__ void __launch_bounds__(kWarps * 32) simt_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
   __shared__ SimtShared<T, D> s;
   constexpr int kPer = D >= 32 ? D / 32 : 1;          // columns of a lane in P V
   constexpr int kVec = 16 / (int)sizeof(T);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Phase& ph = pre ? a.pre : a.own;
+  warm_args(a);
   chain_next();
   sched::Walk w;
   if (!sched::begin(a, pre, blockIdx.x, w)) {         // the block's warps walk alike
@@ -248,7 +249,8 @@ constexpr int kJoinMaxRows = 16;
 constexpr int kChunk = 8;              // at most 16; 10 spilled and took 1 us more
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArgs a, const int rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) 
+    join_kernel(const __grid_constant__ PagedArgs a, const int rows) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
   struct RowPieces {
     int own, own_head, own_next;   // partial results of the own phase, first slots
@@ -260,6 +262,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const PagedArg
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y, in_b = a.c.Hkv * a.TG;
   const int r0 = blockIdx.x * rows, count = min(rows, in_b - r0);
+  warm_args(a);
   if (warp == 0) {
     const sched::Batch t = sched::scan_batch(a, b);
     if (lane < count) {

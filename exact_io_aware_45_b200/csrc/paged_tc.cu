@@ -101,7 +101,7 @@ __device__ __forceinline__ void copy_wait_all() {
 
 template <int D, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
-    tc_kernel(const PagedArgs a, const bool pre, const long long stall) {
+    tc_kernel(const __grid_constant__ PagedArgs a, const bool pre, const long long stall) {
   using C = Cfg<D, kTwo>;
   constexpr uint32_t kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Phase& ph = pre ? a.pre : a.own;
+  warm_args(a);
   chain_next();
   sched::Walk w;
   if (!sched::begin(a, pre, blockIdx.x, w)) {            // the same answer in every warp
