@@ -124,7 +124,11 @@ __device__ __forceinline__ void chain_end() {
 
 // Kernel families. Each runs one phase (`pre`: the shared prefix).
 cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
-constexpr int kSimtRows = 8, kSimtTileLog2 = 5, kSimtBlocksPerSm = 4;
+constexpr int kSimtRows = 4, kSimtTileLog2 = 5, kSimtBlocksPerSm = 4;
+// The same for many packed rows, tiled in registers; a stream is a block.
+cudaError_t paged_fma(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
+constexpr int kFmaRows = 64;
+constexpr int fma_blocks_per_sm(int d) { return d == 128 ? 2 : d == 64 ? 3 : 4; }   // shared memory
 // mma.sync kernel for few packed rows (bf16, d in {64, 128}); a stream is a warp.
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
 constexpr int kMmaRows = 16, kMmaWarps = 4, kMmaBlocksPerSm = 2;

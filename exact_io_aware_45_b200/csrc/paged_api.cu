@@ -88,14 +88,17 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
 }
 
 // Kernels of a phase: bf16 with d of 64 or 128 runs on the tensor cores, all else
-// on the CUDA cores. The mma.sync kernel reads K and V once per kMmaRows packed rows and
+// on the CUDA cores. There the kernel tiled in registers takes 64 rows at once, the other up
+// to four: 64 sequences of 8 rows and 8 heads behind 4,096 tokens (fp32, d 128) take 191 us with
+// the first and 555 with the second, 32 decoding sequences of 8 rows (bf16, d 32) 14 and 18, but 8
+// of 5 rows and 8 heads 41 and 38. The mma.sync kernel reads K and V once per kMmaRows packed rows and
 // is quick with short sequences; the tcgen05 kernel takes 128 or 256 rows at once, which
 // costs an item more to begin and end. At 24 to 32 rows (two row tiles) 64 sequences of 20
 // to 300 tokens take 27 and 42 us, 32 of 100 to 2,000 38 and 45, 8 of 8,192 89 and 68;
 // at 40 the first is at 34, 51 and 122 us, and the second ahead from some hundred tokens on.
-enum Family { kSimt, kMma, kTc };
+enum Family { kSimt, kFma, kMma, kTc };
 Family family(const CacheView& v, int rows) {
-  if (v.row_bytes != 2 * v.d || v.d < 64) return kSimt;
+  if (v.row_bytes != 2 * v.d || v.d < 64) return rows <= kSimtRows ? kSimt : kFma;
   return rows <= 2 * kMmaRows ? kMma : kTc;
 }
 
@@ -108,9 +111,23 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
   int per = 1;           // streams of a block
   switch (family(v, rows)) {
     case kSimt:
-      p.rows = kSimtRows;
+      p.rows = rows <= 2 ? rows : kSimtRows;
       p.tile_log2 = kSimtTileLog2;
       p.n = sms * kSimtBlocksPerSm;
+      // (4, 2, 4 of them: 64 sequences of 1 to 300 tokens 29 us instead of 19)
+      p.over = 3;
+      p.snap = 1;
+      p.least = 2;
+      break;
+    case kFma:
+      p.rows = kFmaRows;
+      p.tile_log2 = kSimtTileLog2;
+      p.n = sms * fma_blocks_per_sm(v.d);
+      // a tile takes a lone block 1.5 us, and beginning little more: 89 sequences of 35 tokens 18
+      // us, 2 with chunks of 64 tokens 30; 31 and 36 with (4, 2, 4)
+      p.over = 1;
+      p.snap = 1;
+      p.least = 1;
       break;
     case kMma:
       p.rows = rows <= 8 ? 8 : kMmaRows;
@@ -143,6 +160,7 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
 cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) {
   switch (family(a.c, pre ? a.B * a.TG : a.TG)) {
     case kSimt: return paged_simt(a, pre, dtype, st);
+    case kFma: return paged_fma(a, pre, dtype, st);
     case kMma: return paged_mma(a, pre, st);
     default: return paged_tc(a, pre, st);
   }

@@ -1,5 +1,5 @@
-// Paged attention on the CUDA cores (fp32 inputs, and head sizes the tensor-core
-// kernels do not take), and the kernel that joins partial results.
+// Paged attention on the CUDA cores for one to four query rows per KV head (fp32 inputs, and head
+// sizes the tensor-core kernels do not take), and the kernel that joins partial results.
 //
 // For each packed query row r of a piece, over the keys j in [lo_r, hi_r):
 //   x_rj = scale q_r . k_j (soft-capped), and the running
@@ -10,8 +10,10 @@
 // reads each V row together with its warp. The four warps of a block
 // take tiles in turn and are merged once per piece.
 //
-// Bound: 4 d rows flops a key in fp32 against 2 d elements read: at 8 rows and
-// fp32 4 flops a byte, above which the CUDA cores (not HBM) are the limit.
+// Bound: the load pipe (each lane reads a row of its own) and latency; more rows per key would
+// need more reads of q and p than multiply-adds can hide, and go to paged_fma.cu. The rows are a
+// template argument, one, two or four: with 8 for all, 16 sequences of 100 to 4,000 tokens (8
+// heads, d 64) took 40 us at one row, 64 of 1 to 300 at four rows 19; now 24 and 14.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -21,7 +23,6 @@
 namespace fa {
 namespace {
 
-constexpr int kRows = kSimtRows;
 constexpr int kTile = 1 << kSimtTileLog2;
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -60,7 +61,7 @@ __device__ __forceinline__ void load_f(const __nv_bfloat16* p, float (&x)[N]) {
 __device__ __forceinline__ void store_f(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
 
-template <typename T, int D>
+template <int D, int kRows>
 struct SimtShared {
   alignas(16) float q[kRows][D];                      // read as float4
   float p[kWarps][kRows][kTile];
@@ -70,9 +71,10 @@ struct SimtShared {
   int out[kRows];
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) simt_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
-  __shared__ SimtShared<T, D> s;
+template <typename T, int D, int kRows>
+__global__ void __launch_bounds__(kWarps * 32)
+    simt_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
+  __shared__ SimtShared<D, kRows> s;
   constexpr int kPer = D >= 32 ? D / 32 : 1;          // columns of a lane in P V
   constexpr int kVec = 16 / (int)sizeof(T);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -220,18 +222,20 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const __grid_constant
 
 template <typename T, int D>
 cudaError_t launch_simt(const PagedArgs& a, bool pre, cudaStream_t st) {
-  return launch_chained(simt_kernel<T, D>, (pre ? a.pre : a.own).n, kWarps * 32, 0, st,
-                        !pre && a.shared, a, pre);
+  const Phase& ph = pre ? a.pre : a.own;
+  const auto kernel = ph.rows == 1 ? simt_kernel<T, D, 1> : ph.rows == 2 ? simt_kernel<T, D, 2>
+                                                                         : simt_kernel<T, D, 4>;
+  return launch_chained(kernel, ph.n, kWarps * 32, 0, st, !pre && a.shared, a, pre);
 }
 
 template <typename T>
 cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
-  switch (a.c.d) {
-    case 16: return launch_simt<T, 16>(a, pre, st);
-    case 32: return launch_simt<T, 32>(a, pre, st);
-    case 64: return launch_simt<T, 64>(a, pre, st);
-    default: return launch_simt<T, 128>(a, pre, st);
+  if (a.c.d == 16) return launch_simt<T, 16>(a, pre, st);
+  if constexpr (sizeof(T) == 4) {                       // bf16 has the tensor cores from 64 on
+    if (a.c.d == 64) return launch_simt<T, 64>(a, pre, st);
+    if (a.c.d == 128) return launch_simt<T, 128>(a, pre, st);
   }
+  return launch_simt<T, 32>(a, pre, st);
 }
 
 // ---------------------------------------------------------------- join

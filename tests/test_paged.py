@@ -344,6 +344,31 @@ def test_shared_rows_in_one_and_two_tiles(d, B, T, wl, causal, cap, scale):
                 wl=wl, causal=causal, cap=cap, scale=scale)
 
 
+CUDA_CORES = [("f32", 128), ("f32", 64), ("f32", 32), ("f32", 16), ("bf16", 32), ("bf16", 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", CUDA_CORES)
+@pytest.mark.parametrize("T,G", [(1, 2), (3, 1), (4, 1), (5, 1), (1, 16), (17, 1), (16, 4), (13, 5),
+                                 (50, 3)])
+def test_paged_rows_on_the_cuda_cores(dtype, d, T, G):
+    """One to four rows, part of a tile of 64, one tile, several; masks that leave rows empty."""
+    lens = [0, 1, 15, 31, 32, 33, 100, 401]
+    attend_case(lens, 2 * G, 2, d, 16, dtype, T=T)
+    attend_case(lens, 2 * G, 2, d, 32, dtype, T=T, wl=20, cap=15.0, layers=2, layer=1,
+                layout="joined")
+    attend_case(lens, 2 * G, 2, d, 128, dtype, T=T, wl=7, causal=False, scale=-0.3, layout="inside")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", CUDA_CORES)
+@pytest.mark.parametrize("B,T,shared", [(3, 1, 64), (16, 1, 480), (17, 4, 160), (70, 1, 1024)])
+def test_shared_rows_on_the_cuda_cores(dtype, d, B, T, shared):
+    lens = [shared - 20 + (11 * b * b) % 150 for b in range(B)]
+    attend_case(lens, 4, 1, d, 32, dtype, T=T, shared=shared)
+    attend_case(lens, 4, 1, d, 32, dtype, T=T, shared=shared, wl=shared - 40, cap=20.0)
+
+
 @pytest.mark.gpu
 def test_paged_many_sequences():
     """More sequences than threads of a block that scans their lengths."""
