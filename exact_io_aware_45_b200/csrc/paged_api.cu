@@ -91,15 +91,15 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
 // on the CUDA cores. There the kernel tiled in registers takes 64 rows at once, the other up
 // to four: 64 sequences of 8 rows and 8 heads behind 4,096 tokens (fp32, d 128) take 191 us with
 // the first and 555 with the second, 32 decoding sequences of 8 rows (bf16, d 32) 14 and 18, but 8
-// of 5 rows and 8 heads 41 and 38. The mma.sync kernel reads K and V once per kMmaRows packed rows and
-// is quick with short sequences; the tcgen05 kernel takes 128 or 256 rows at once, which
-// costs an item more to begin and end. At 24 to 32 rows (two row tiles) 64 sequences of 20
-// to 300 tokens take 27 and 42 us, 32 of 100 to 2,000 38 and 45, 8 of 8,192 89 and 68;
-// at 40 the first is at 34, 51 and 122 us, and the second ahead from some hundred tokens on.
+// of 5 rows and 8 heads 41 and 38. The mma.sync kernel reads K and V once per 16 or 24 packed rows
+// and is quick with short sequences; the tcgen05 kernel takes 128 or 256 rows at once, which
+// costs an item more to begin and end. At 32 rows (two row tiles, d 128) 64 sequences of 20
+// to 300 tokens take 29 and 43 us, 32 of 100 to 2,000 38 and 43, 8 of 8,192 90 and 65; at 40
+// the first is at 34, 51 and 122 us, and the second ahead from some hundred tokens on.
 enum Family { kSimt, kFma, kMma, kTc };
 Family family(const CacheView& v, int rows) {
   if (v.row_bytes != 2 * v.d || v.d < 64) return rows <= kSimtRows ? kSimt : kFma;
-  return rows <= 2 * kMmaRows ? kMma : kTc;
+  return rows <= kMmaMost ? kMma : kTc;
 }
 
 // The work division of a phase of `groups` sequences and KV heads with `rows`
@@ -130,7 +130,10 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
       p.least = 1;
       break;
     case kMma:
-      p.rows = rows <= 8 ? 8 : kMmaRows;
+      // 17 to 24 rows are one tile where the heads alone fill the GPU (8 sequences of 8,192
+      // tokens, 8 heads, d 128: 56 us, 84 as two of 16), else two, for latency (one of 3,000, 4
+      // heads: 12.7 us, 14.3 as one). Tiles of 32 spill at d 128 and gained little at 64.
+      p.rows = rows <= 8 ? 8 : rows > 16 && rows <= 24 && groups >= 32 ? 24 : 16;
       p.tile_log2 = mma_tile_log2(v.d);
       per = kMmaWarps;
       p.n = sms * kMmaWarps * kMmaBlocksPerSm;

@@ -383,12 +383,19 @@ cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
                         kSmem, st, !pre && a.shared, a, pre);
 }
 
+template <int D>
+cudaError_t launch_d(const PagedArgs& a, bool pre, cudaStream_t st) {
+  switch ((pre ? a.pre : a.own).rows / 8) {
+    case 1: return launch<D, 1>(a, pre, st);
+    case 2: return launch<D, 2>(a, pre, st);
+    default: return launch<D, 3>(a, pre, st);
+  }
+}
+
 }  // namespace
 
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st) {
-  const bool wide = (pre ? a.pre : a.own).rows > 8;
-  if (a.c.d == 128) return wide ? launch<128, 2>(a, pre, st) : launch<128, 1>(a, pre, st);
-  return wide ? launch<64, 2>(a, pre, st) : launch<64, 1>(a, pre, st);
+  return a.c.d == 128 ? launch_d<128>(a, pre, st) : launch_d<64>(a, pre, st);
 }
 
 }  // namespace fa

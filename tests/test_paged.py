@@ -344,6 +344,19 @@ def test_shared_rows_in_one_and_two_tiles(d, B, T, wl, causal, cap, scale):
                 wl=wl, causal=causal, cap=cap, scale=scale)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,G,wl,cap,causal", [(3, 8, -1, 0.0, True), (4, 5, 30, 0.0, True),
+                                               (17, 1, -1, 20.0, False), (23, 1, 5, 10.0, True)])
+def test_paged_row_tiles_of_24(d, T, G, wl, cap, causal):
+    """17 to 24 rows with many heads in the batch, with few, and behind a prefix."""
+    lens = [0, 1, 16, 17, 100, 255, 256, 700, 33, 1500]
+    attend_case(lens, 4 * G, 4, d, 16, "bf16", T=T, wl=wl, cap=cap, causal=causal)
+    attend_case(lens[4:7], 2 * G, 2, d, 64, "bf16", T=T, wl=wl, cap=cap, causal=causal)
+    attend_case([64 + n for n in lens], 4 * G, 4, d, 32, "bf16", T=T, shared=64, wl=wl, cap=cap,
+                causal=causal)
+
+
 CUDA_CORES = [("f32", 128), ("f32", 64), ("f32", 32), ("f32", 16), ("bf16", 32), ("bf16", 16)]
 
 
