@@ -93,13 +93,15 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
 // the first and 555 with the second, 32 decoding sequences of 8 rows (bf16, d 32) 14 and 18, but 8
 // of 5 rows and 8 heads 41 and 38. The mma.sync kernel reads K and V once per 16 or 24 packed rows
 // and is quick with short sequences; the tcgen05 kernel takes 128 or 256 rows at once, which
-// costs an item more to begin and end. At 32 rows (two row tiles, d 128) 64 sequences of 20
-// to 300 tokens take 29 and 43 us, 32 of 100 to 2,000 38 and 43, 8 of 8,192 90 and 65; at 40
-// the first is at 34, 51 and 122 us, and the second ahead from some hundred tokens on.
+// costs an item more to begin and end. Two row tiles (25 to 32 rows) of d 128 bind the first by
+// its work, so the second has them where a sequence may be long (`keys`: what its table can
+// hold): 64 sequences of 20 to 300 tokens take 29 and 43 us, 32 of 100 to 2,000 37 and 44, 80 of
+// 1,562 (behind 2,144 shared) 285 and 200, 8 of 8,192 91 and 66. At d 64 they are level.
 enum Family { kSimt, kFma, kMma, kTc };
-Family family(const CacheView& v, int rows) {
+Family family(const CacheView& v, int rows, long long keys) {
   if (v.row_bytes != 2 * v.d || v.d < 64) return rows <= kSimtRows ? kSimt : kFma;
-  return rows <= kMmaMost ? kMma : kTc;
+  const bool twice = rows > 24 && v.d == 128;            // two row tiles that are bound by their work
+  return rows <= kMmaMost && !(twice && keys > 1024) ? kMma : kTc;
 }
 
 // The work division of a phase of `groups` sequences and KV heads with `rows`
@@ -109,7 +111,7 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
   Phase p;
   p.sms = sms;
   int per = 1;           // streams of a block
-  switch (family(v, rows)) {
+  switch (family(v, rows, keys)) {
     case kSimt:
       p.rows = rows <= 2 ? rows : kSimtRows;
       p.tile_log2 = kSimtTileLog2;
@@ -160,8 +162,14 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
   return p;
 }
 
+// Behind the prefix a sequence has at most what its table holds.
+Family own_family(const PagedArgs& a) {
+  return family(a.c, a.TG, ((long long)a.c.width << a.c.page_log2) - a.shared);
+}
+Family pre_family(const PagedArgs& a) { return family(a.c, a.B * a.TG, a.shared); }
+
 cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) {
-  switch (family(a.c, pre ? a.B * a.TG : a.TG)) {
+  switch (pre ? pre_family(a) : own_family(a)) {
     case kSimt: return paged_simt(a, pre, dtype, st);
     case kFma: return paged_fma(a, pre, dtype, st);
     case kMma: return paged_mma(a, pre, st);
@@ -172,12 +180,12 @@ cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) 
 // Fills in both phases; false if their units or partial rows do not fit an int.
 bool plan(PagedArgs& a, int sms) {
   const long long keys = (long long)a.c.width << a.c.page_log2;
-  a.own = divide(a.c, a.B * a.c.Hkv, a.TG, keys, sms);
+  a.own = divide(a.c, a.B * a.c.Hkv, a.TG, keys - a.shared, sms);
   a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, a.shared, sms) : Phase();
   // The tcgen05 kernel leaves the memory idle and the mma.sync kernel the tensor cores: they
   // run side by side on different SMs. A tile of 256 rows takes an SM 2.2 us, 8 KB of an own
   // stream 0.14 us.
-  if (a.shared && family(a.c, a.B * a.TG) == kTc && family(a.c, a.TG) == kMma)
+  if (a.shared && pre_family(a) == kTc && own_family(a) == kMma)
     a.pre.yield = a.pre.rows == kTcRows ? 8 : 16;
   const long long most = keys / 16 + 8;
   for (const Phase* p : {&a.own, &a.pre})

@@ -357,6 +357,18 @@ def test_paged_row_tiles_of_24(d, T, G, wl, cap, causal):
                 causal=causal)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,G", [(4, 8), (29, 1), (5, 5)])
+@pytest.mark.parametrize("longest", [900, 2500])
+def test_paged_two_row_tiles(d, T, G, longest):
+    """25 to 32 rows, over tables for short and for long sequences, alone and behind a prefix."""
+    lens = [0, 1, 31, 128, 129, 500, longest]
+    attend_case(lens, 2 * G, 2, d, 16, "bf16", T=T, wl=200)
+    attend_case([640 + n for n in lens], 2 * G, 2, d, 128, "bf16", T=T, shared=640, cap=25.0)
+    attend_case([1280, 1300], 2 * G, 2, d, 64, "bf16", T=T, shared=1280)
+
+
 CUDA_CORES = [("f32", 128), ("f32", 64), ("f32", 32), ("f32", 16), ("bf16", 32), ("bf16", 16)]
 
 
