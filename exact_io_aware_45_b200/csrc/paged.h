@@ -124,7 +124,8 @@ __device__ __forceinline__ void chain_end() {
 
 // Kernel families. Each runs one phase (`pre`: the shared prefix).
 cudaError_t paged_simt(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
-constexpr int kSimtRows = 4, kSimtTileLog2 = 5, kSimtBlocksPerSm = 4;
+constexpr int kSimtRows = 4, kSimtTileLog2 = 5;
+constexpr int simt_blocks_per_sm(int d, int rows) { return d * rows >= 512 ? 3 : 4; }  // registers
 // The same for many packed rows, tiled in registers; a stream is a block.
 cudaError_t paged_fma(const PagedArgs& a, bool pre, int dtype, cudaStream_t st);
 constexpr int kFmaRows = 64;

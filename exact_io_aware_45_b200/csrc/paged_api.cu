@@ -115,7 +115,7 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
     case kSimt:
       p.rows = rows <= 2 ? rows : kSimtRows;
       p.tile_log2 = kSimtTileLog2;
-      p.n = sms * kSimtBlocksPerSm;
+      p.n = sms * simt_blocks_per_sm(v.d, p.rows);
       // (4, 2, 4 of them: 64 sequences of 1 to 300 tokens 29 us instead of 19)
       p.over = 3;
       p.snap = 1;

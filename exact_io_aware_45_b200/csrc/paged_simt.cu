@@ -4,16 +4,19 @@
 // For each packed query row r of a piece, over the keys j in [lo_r, hi_r):
 //   x_rj = scale q_r . k_j (soft-capped), and the running
 //   m = max(m, max_j x_rj), l = e^(m_old - m) l + sum_j e^(x_rj - m), likewise O,
-// in base 2. A warp takes tiles of 32 keys. For the scores a lane owns a key:
-// it reads its row in 16-byte pieces and the query rows from shared memory, so
-// no score needs a reduction across lanes; for P V a lane owns d / 32 columns and
-// reads each V row together with its warp. The four warps of a block
-// take tiles in turn and are merged once per piece.
+// in base 2. A warp takes tiles of 32 keys. For the scores up to eight lanes read a key's row
+// side by side, 16 bytes each, against their part of the query rows in registers; the sums over
+// these lanes are exchanged so that each lane ends with the scores of one key (7 shuffles a row and
+// tile). For P V a lane owns d / 32 columns and reads each V row together with its warp. The
+// four warps of a block take tiles in turn and are merged once per piece.
 //
-// Bound: the load pipe (each lane reads a row of its own) and latency; more rows per key would
-// need more reads of q and p than multiply-adds can hide, and go to paged_fma.cu. The rows are a
-// template argument, one, two or four: with 8 for all, 16 sequences of 100 to 4,000 tokens (8
-// heads, d 64) took 40 us at one row, 64 of 1 to 300 at four rows 19; now 24 and 14.
+// (A lane per key needs no sums across lanes, but reads 32 rows at once, half a sector of each: 64
+// sequences of 1,000 to 3,000 tokens, 8 heads, fp32, took 190 us at d 16, now 52, and 16 of 50 to
+// 4,000 at d 128 43, now 30.)
+//
+// Bound: HBM for one row and long sequences (64 of 1,000 to 3,000 tokens, 8/8 heads, 2 rows, d
+// 128, fp32: 1 GB in 171 us), latency for short ones, multiply-adds in between. The rows are a
+// template argument, one, two or four: more go to paged_fma.cu.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -63,8 +66,7 @@ __device__ __forceinline__ void store_f(__nv_bfloat16* p, float x) { *p = __floa
 
 template <int D, int kRows>
 struct SimtShared {
-  alignas(16) float q[kRows][D];                      // read as float4
-  float p[kWarps][kRows][kTile];
+  alignas(16) float p[kWarps][kRows][kTile];          // read as float4
   float o[kWarps][kRows][D];
   float m[kWarps][kRows], l[kWarps][kRows];
   int lo[kRows], hi[kRows];
@@ -72,12 +74,17 @@ struct SimtShared {
 };
 
 template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
     simt_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
   __shared__ SimtShared<D, kRows> s;
   constexpr int kPer = D >= 32 ? D / 32 : 1;          // columns of a lane in P V
-  constexpr int kVec = 16 / (int)sizeof(T);
+  // 16-byte pieces: kLanes lanes read kLanes x 16 bytes of a key side by side, kChunks times
+  constexpr int kVec = 16 / (int)sizeof(T), kPieces = D / kVec;
+  constexpr int kLanes = kPieces < 8 ? kPieces : 8, kChunks = kPieces / kLanes;
+  constexpr int kSide = 32 / kLanes;                  // keys side by side
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int part = lane % kLanes, side = lane / kLanes;
+  const int mine_key = part * kSide + side;           // whose scores this lane ends up with
   const Phase& ph = pre ? a.pre : a.own;
   warm_args(a);
   chain_next();
@@ -97,17 +104,20 @@ __global__ void __launch_bounds__(kWarps * 32)
       s.lo[tid] = r.lo, s.hi[tid] = r.hi, s.out[tid] = r.out;
     }
     __syncthreads();
-    for (int i = tid; i < kRows * D; i += kWarps * 32) {
-      const int r = i / D;
-      float x = 0.f;
-      if (r < pc.rows) {
-        float y[1];
-        load_f<1>(Q + (size_t)s.out[r] * D + i % D, y);
-        x = y[0] * a.scale;
+    float q[kRows][kChunks][kVec];                      // this lane's part, scaled
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (r < pc.rows) {
+          load_f<kVec>(Q + (size_t)s.out[r] * D + (c * kLanes + part) * kVec, q[r][c]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) q[r][c][v] = 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) q[r][c][v] *= a.scale;
       }
-      s.q[r][i % D] = x;
-    }
-    __syncthreads();
     float m[kRows], l[kRows], o[kRows][kPer];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -116,34 +126,61 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int i = 0; i < kPer; ++i) o[r][i] = 0.f;
     }
     const int* trow = sched::table_row(a, pc.table);
+    const long long head = (long long)pc.h * a.c.head_bytes;
+    // pages of a tile's halves (a page has 16 keys at least), asked for one tile ahead
+    int page0, page1;
+    auto find = [&](int t) {
+      const int j = t * kTile;
+      page0 = j < pc.hi ? __ldg(trow + (j >> a.c.page_log2)) : 0;
+      page1 = j + 16 < pc.hi ? __ldg(trow + ((j + 16) >> a.c.page_log2)) : 0;
+    };
+    auto offset = [&](int page, int j) {              // of key j in this page
+      if ((unsigned)page >= (unsigned)a.c.pages) page = 0;
+      return page * a.c.page_stride + head +
+             (long long)(j & ((1 << a.c.page_log2) - 1)) * a.c.row_bytes;
+    };
+    find(pc.t0 + warp);
     for (int t = pc.t0 + warp; t < pc.t1; t += kWarps) {
-      const int j = t * kTile + lane;
+      const int j0 = t * kTile, j = j0 + mine_key;
       const bool in = j >= pc.lo && j < pc.hi;
-      const long long off = in ? sched::key_offset(a.c, trow, pc.h, j) : 0;
-      float x[kRows];
+      const long long off0 = offset(page0, j0), off1 = offset(page1, j0 + 16);
+      find(t + kWarps);
+      float x[kLanes][kRows];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) x[r] = 0.f;
-      if (in) {
-        const T* k = reinterpret_cast<const T*>(a.K + off);
+      for (int g = 0; g < kLanes; ++g) {
 #pragma unroll
-        for (int i = 0; i < D; i += kVec) {
-          float kv[kVec];
-          load_f<kVec>(k + i, kv);
+        for (int r = 0; r < kRows; ++r) x[g][r] = 0.f;
+        const int i = g * kSide + side;
+        const T* k = reinterpret_cast<const T*>(
+                         a.K + (g * kSide < 16 ? off0 + i * a.c.row_bytes
+                                               : off1 + (i - 16) * a.c.row_bytes)) + part * kVec;
+        if (j0 + i >= pc.lo && j0 + i < pc.hi) {
 #pragma unroll
-          for (int r = 0; r < kRows; ++r)
+          for (int c = 0; c < kChunks; ++c) {
+            float kv[kVec];
+            load_f<kVec>(k + c * kLanes * kVec, kv);
 #pragma unroll
-            for (int v = 0; v < kVec; v += 4) {
-              const float4 qv = *reinterpret_cast<const float4*>(&s.q[r][i + v]);
-              x[r] = fmaf(qv.x, kv[v], x[r]);
-              x[r] = fmaf(qv.y, kv[v + 1], x[r]);
-              x[r] = fmaf(qv.z, kv[v + 2], x[r]);
-              x[r] = fmaf(qv.w, kv[v + 3], x[r]);
-            }
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+              for (int v = 0; v < kVec; ++v) x[g][r] = fmaf(q[r][c][v], kv[v], x[g][r]);
+          }
         }
       }
+      // sums over the kLanes lanes of a key, each lane ending with one of kLanes keys
+#pragma unroll
+      for (int half = kLanes / 2; half; half >>= 1)
+#pragma unroll
+        for (int g = 0; g < half; ++g)
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const bool up = part & half;
+            const float give = up ? x[g][r] : x[g + half][r];
+            const float keep = up ? x[g + half][r] : x[g][r];
+            x[g][r] = keep + __shfl_xor_sync(~0u, give, half);
+          }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        float y = x[r];
+        float y = x[0][r];
         if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
         y *= kLog2e;
         if (!(in && j >= s.lo[r] && j < s.hi[r])) y = -INFINITY;
@@ -160,27 +197,36 @@ __global__ void __launch_bounds__(kWarps * 32)
         l[r] = l[r] * c + sum;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) o[r][i] *= c;
-        s.p[warp][r][lane] = e;
+        s.p[warp][r][mine_key] = e;
       }
       __syncwarp();
       const bool mine = lane * kPer < D;
-#pragma unroll 4
-      for (int i = 0; i < kTile; ++i) {
-        const long long vo = __shfl_sync(~0u, off, i);
-        if (!__shfl_sync(~0u, (int)in, i)) continue;   // what no row sees is not read
-        float v[kPer];
-        if (mine) {
-          load_f<kPer>(reinterpret_cast<const T*>(a.V + vo) + lane * kPer, v);
-        } else {
+#pragma unroll 2
+      for (int i = 0; i < kTile; i += 4) {
+        float p[kRows][4], v[4][kPer];
+        const char* from = a.V + (i < 16 ? off0 + i * a.c.row_bytes
+                                         : off1 + (i - 16) * a.c.row_bytes);
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) v[e] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          // what no row sees is not read
+          if (mine && j0 + i + k >= pc.lo && j0 + i + k < pc.hi) {
+            load_f<kPer>(reinterpret_cast<const T*>(from + k * a.c.row_bytes) + lane * kPer, v[k]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
+          }
         }
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-          const float p = s.p[warp][r][i];
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) o[r][e] = fmaf(p, v[e], o[r][e]);
+          const float4 x4 = *reinterpret_cast<const float4*>(&s.p[warp][r][i]);
+          p[r][0] = x4.x, p[r][1] = x4.y, p[r][2] = x4.z, p[r][3] = x4.w;
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[r][e] = fmaf(p[r][k], v[k][e], o[r][e]);
       }
       __syncwarp();
     }
