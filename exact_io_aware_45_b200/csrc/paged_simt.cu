@@ -12,11 +12,12 @@
 //
 // (A lane per key needs no sums across lanes, but reads 32 rows at once, half a sector of each: 64
 // sequences of 1,000 to 3,000 tokens, 8 heads, fp32, took 190 us at d 16, now 52, and 16 of 50 to
-// 4,000 at d 128 43, now 30.)
+// 4,000 at d 128 43, now 26.)
 //
-// Bound: HBM for one row and long sequences (64 of 1,000 to 3,000 tokens, 8/8 heads, 2 rows, d
-// 128, fp32: 1 GB in 171 us), latency for short ones, multiply-adds in between. The rows are a
-// template argument, one, two or four: more go to paged_fma.cu.
+// Bound: HBM for long sequences (64 of 1,000 to 3,000 tokens, 8 heads, d 128, fp32, 1 GB: 175 us
+// with two rows, 180 with four), latency for short ones. The rows are a template argument, one,
+// two or four: more go to paged_fma.cu. Four rows of d 128 are read from shared memory (in
+// registers they spilled, 304 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -64,8 +65,13 @@ __device__ __forceinline__ void load_f(const __nv_bfloat16* p, float (&x)[N]) {
 __device__ __forceinline__ void store_f(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
 
+// The query rows in shared memory where registers would not hold them.
+template <int D, int kRows>
+constexpr bool kShareQ = D * kRows >= 512;
+
 template <int D, int kRows>
 struct SimtShared {
+  alignas(16) float q[kShareQ<D, kRows> ? kRows : 1][kShareQ<D, kRows> ? D : 4];
   alignas(16) float p[kWarps][kRows][kTile];          // read as float4
   float o[kWarps][kRows][D];
   float m[kWarps][kRows], l[kWarps][kRows];
@@ -82,6 +88,8 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
   constexpr int kVec = 16 / (int)sizeof(T), kPieces = D / kVec;
   constexpr int kLanes = kPieces < 8 ? kPieces : 8, kChunks = kPieces / kLanes;
   constexpr int kSide = 32 / kLanes;                  // keys side by side
+  constexpr int kRowBytes = D * (int)sizeof(T);
+  constexpr int kHeld = kShareQ<D, kRows> ? 1 : kChunks;   // chunks of Q in registers
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part = lane % kLanes, side = lane / kLanes;
   const int mine_key = part * kSide + side;           // whose scores this lane ends up with
@@ -104,20 +112,29 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
       s.lo[tid] = r.lo, s.hi[tid] = r.hi, s.out[tid] = r.out;
     }
     __syncthreads();
-    float q[kRows][kChunks][kVec];                      // this lane's part, scaled
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (r < pc.rows) {
-          load_f<kVec>(Q + (size_t)s.out[r] * D + (c * kLanes + part) * kVec, q[r][c]);
-        } else {
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) q[r][c][v] = 0.f;
-        }
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) q[r][c][v] *= a.scale;
+    float q[kRows][kHeld][kVec];                        // this lane's part, scaled
+    if constexpr (kShareQ<D, kRows>) {
+      for (int i = tid; i < kRows * D; i += kWarps * 32) {
+        float x[1] = {0.f};
+        if (i / D < pc.rows) load_f<1>(Q + (size_t)s.out[i / D] * D + i % D, x);
+        s.q[i / D][i % D] = x[0] * a.scale;
       }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (r < pc.rows) {
+            load_f<kVec>(Q + (size_t)s.out[r] * D + (c * kLanes + part) * kVec, q[r][c]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) q[r][c][v] = 0.f;
+          }
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) q[r][c][v] *= a.scale;
+        }
+    }
     float m[kRows], l[kRows], o[kRows][kPer];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -137,7 +154,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
     auto offset = [&](int page, int j) {              // of key j in this page
       if ((unsigned)page >= (unsigned)a.c.pages) page = 0;
       return page * a.c.page_stride + head +
-             (long long)(j & ((1 << a.c.page_log2) - 1)) * a.c.row_bytes;
+             (long long)(j & ((1 << a.c.page_log2) - 1)) * kRowBytes;
     };
     find(pc.t0 + warp);
     for (int t = pc.t0 + warp; t < pc.t1; t += kWarps) {
@@ -147,24 +164,40 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
       find(t + kWarps);
       float x[kLanes][kRows];
 #pragma unroll
-      for (int g = 0; g < kLanes; ++g) {
+      for (int g = 0; g < kLanes; ++g)
 #pragma unroll
         for (int r = 0; r < kRows; ++r) x[g][r] = 0.f;
-        const int i = g * kSide + side;
-        const T* k = reinterpret_cast<const T*>(
-                         a.K + (g * kSide < 16 ? off0 + i * a.c.row_bytes
-                                               : off1 + (i - 16) * a.c.row_bytes)) + part * kVec;
-        if (j0 + i >= pc.lo && j0 + i < pc.hi) {
+      const char* k0 = a.K + off0 + side * kRowBytes + part * 16;
+      const char* k1 = a.K + off1 + side * kRowBytes + part * 16;
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            float kv[kVec];
-            load_f<kVec>(k + c * kLanes * kVec, kv);
+      for (int c = 0; c < kChunks; ++c) {
+        const int held = kShareQ<D, kRows> ? 0 : c;
+        if constexpr (kShareQ<D, kRows>) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
-#pragma unroll
-              for (int v = 0; v < kVec; ++v) x[g][r] = fmaf(q[r][c][v], kv[v], x[g][r]);
+          for (int r = 0; r < kRows; ++r) {
+            const float4 x4 = *reinterpret_cast<const float4*>(&s.q[r][(c * kLanes + part) * 4]);
+            q[r][0][0] = x4.x, q[r][0][1] = x4.y, q[r][0][2] = x4.z, q[r][0][3] = x4.w;
           }
         }
+        float kv[kLanes][kVec];
+#pragma unroll
+        for (int g = 0; g < kLanes; ++g) {
+          const int i = g * kSide + side;
+          const char* from = g < kLanes / 2 ? k0 + g * kSide * kRowBytes
+                                            : k1 + (g - kLanes / 2) * kSide * kRowBytes;
+          if (j0 + i >= pc.lo && j0 + i < pc.hi) {
+            load_f<kVec>(reinterpret_cast<const T*>(from + c * kLanes * 16), kv[g]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) kv[g][v] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < kLanes; ++g)
+#pragma unroll
+          for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) x[g][r] = fmaf(q[r][held][v], kv[g][v], x[g][r]);
       }
       // sums over the kLanes lanes of a key, each lane ending with one of kLanes keys
 #pragma unroll
@@ -204,13 +237,12 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
 #pragma unroll 2
       for (int i = 0; i < kTile; i += 4) {
         float p[kRows][4], v[4][kPer];
-        const char* from = a.V + (i < 16 ? off0 + i * a.c.row_bytes
-                                         : off1 + (i - 16) * a.c.row_bytes);
+        const char* from = a.V + (i < 16 ? off0 + i * kRowBytes : off1 + (i - 16) * kRowBytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           // what no row sees is not read
           if (mine && j0 + i + k >= pc.lo && j0 + i + k < pc.hi) {
-            load_f<kPer>(reinterpret_cast<const T*>(from + k * a.c.row_bytes) + lane * kPer, v[k]);
+            load_f<kPer>(reinterpret_cast<const T*>(from + k * kRowBytes) + lane * kPer, v[k]);
           } else {
 #pragma unroll
             for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
