@@ -132,7 +132,7 @@ constexpr int kFmaRows = 64;
 constexpr int fma_blocks_per_sm(int d) { return d == 128 ? 2 : d == 64 ? 3 : 4; }   // shared memory
 // mma.sync kernel for few packed rows (bf16, d in {64, 128}); a stream is a warp.
 cudaError_t paged_mma(const PagedArgs& a, bool pre, cudaStream_t st);
-constexpr int kMmaMost = 32, kMmaWarps = 4, kMmaBlocksPerSm = 2;
+constexpr int kMmaWarps = 4, kMmaBlocksPerSm = 2;
 constexpr int mma_tile_log2(int d) { return d == 128 ? 4 : 5; }
 // tcgen05 kernel for many packed rows (bf16, d in {64, 128}); a stream is a CTA.
 // Items of 128 rows (one query tile, its key tiles dealt to two warpgroups) or 256.

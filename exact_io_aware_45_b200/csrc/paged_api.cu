@@ -97,21 +97,32 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
 // its work, so the second has them where a sequence may be long (`keys`: what its table can
 // hold): 64 sequences of 20 to 300 tokens take 29 and 43 us, 32 of 100 to 2,000 37 and 44, 80 of
 // 1,562 (behind 2,144 shared) 285 and 200, 8 of 8,192 91 and 66. At d 64 they are level.
+// Where nothing can be long, up to 64 rows are quicker in tiles of 16 or 24: 61 sequences of
+// 40 rows and 8 heads with 1 to 49 tokens behind 128 shared take 41 us, 74 with an item each.
 enum Family { kSimt, kFma, kMma, kTc };
 Family family(const CacheView& v, int rows, long long keys) {
   if (v.row_bytes != 2 * v.d || v.d < 64) return rows <= kSimtRows ? kSimt : kFma;
-  const bool twice = rows > 24 && v.d == 128;            // two row tiles that are bound by their work
-  return rows <= kMmaMost && !(twice && keys > 1024) ? kMma : kTc;
+  const int most = keys <= 256 ? 64 : v.d == 64 || keys <= 1024 ? 32 : 24;
+  return rows <= most ? kMma : kTc;
+}
+
+// Behind the prefix a sequence has at most what its table holds.
+Family own_family(const PagedArgs& a) {
+  return family(a.c, a.TG, ((long long)a.c.width << a.c.page_log2) - a.shared);
+}
+// A short prefix has few items, which the tcgen05 kernel begins side by side.
+Family pre_family(const PagedArgs& a) {
+  return family(a.c, a.B * a.TG, a.shared < 512 ? 512 : a.shared);
 }
 
 // The work division of a phase of `groups` sequences and KV heads with `rows`
 // packed rows each, over `keys` keys at most. It depends on sizes and types only, so the
 // workspace query and the call agree.
-Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) {
+Phase divide(const CacheView& v, Family kind, int groups, int rows, long long keys, int sms) {
   Phase p;
   p.sms = sms;
   int per = 1;           // streams of a block
-  switch (family(v, rows, keys)) {
+  switch (kind) {
     case kSimt:
       p.rows = rows <= 2 ? rows : kSimtRows;
       p.tile_log2 = kSimtTileLog2;
@@ -135,7 +146,7 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
       // 17 to 24 rows are one tile where the heads alone fill the GPU (8 sequences of 8,192
       // tokens, 8 heads, d 128: 56 us, 84 as two of 16), else two, for latency (one of 3,000, 4
       // heads: 12.7 us, 14.3 as one). Tiles of 32 spill at d 128 and gained little at 64.
-      p.rows = rows <= 8 ? 8 : rows > 16 && rows <= 24 && groups >= 32 ? 24 : 16;
+      p.rows = rows <= 8 ? 8 : groups >= 32 && (rows + 23) / 24 < (rows + 15) / 16 ? 24 : 16;
       p.tile_log2 = mma_tile_log2(v.d);
       per = kMmaWarps;
       p.n = sms * kMmaWarps * kMmaBlocksPerSm;
@@ -162,12 +173,6 @@ Phase divide(const CacheView& v, int groups, int rows, long long keys, int sms) 
   return p;
 }
 
-// Behind the prefix a sequence has at most what its table holds.
-Family own_family(const PagedArgs& a) {
-  return family(a.c, a.TG, ((long long)a.c.width << a.c.page_log2) - a.shared);
-}
-Family pre_family(const PagedArgs& a) { return family(a.c, a.B * a.TG, a.shared); }
-
 cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) {
   switch (pre ? pre_family(a) : own_family(a)) {
     case kSimt: return paged_simt(a, pre, dtype, st);
@@ -180,8 +185,8 @@ cudaError_t run_phase(const PagedArgs& a, bool pre, int dtype, cudaStream_t st) 
 // Fills in both phases; false if their units or partial rows do not fit an int.
 bool plan(PagedArgs& a, int sms) {
   const long long keys = (long long)a.c.width << a.c.page_log2;
-  a.own = divide(a.c, a.B * a.c.Hkv, a.TG, keys - a.shared, sms);
-  a.pre = a.shared ? divide(a.c, a.c.Hkv, a.B * a.TG, a.shared, sms) : Phase();
+  a.own = divide(a.c, own_family(a), a.B * a.c.Hkv, a.TG, keys - a.shared, sms);
+  if (a.shared) a.pre = divide(a.c, pre_family(a), a.c.Hkv, a.B * a.TG, a.shared, sms);
   // The tcgen05 kernel leaves the memory idle and the mma.sync kernel the tensor cores: they
   // run side by side on different SMs. A tile of 256 rows takes an SM 2.2 us, 8 KB of an own
   // stream 0.14 us.

@@ -369,6 +369,17 @@ def test_paged_two_row_tiles(d, T, G, longest):
     attend_case([1280, 1300], 2 * G, 2, d, 64, "bf16", T=T, shared=1280)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,G", [(8, 5), (8, 8), (33, 1), (12, 4), (13, 5)])
+@pytest.mark.parametrize("B", [3, 40])
+def test_paged_many_rows_of_short_sequences(d, T, G, B):
+    """33 to 65 rows where no table can hold more than 256 keys, alone and behind a prefix."""
+    lens = [(13 * b * b + 7 * b) % 200 for b in range(B)]
+    attend_case(lens, G, 1, d, 16, "bf16", T=T, wl=50, cap=25.0)
+    attend_case([128 + n for n in lens], 2 * G, 2, d, 32, "bf16", T=T, shared=128)
+
+
 CUDA_CORES = [("f32", 128), ("f32", 64), ("f32", 32), ("f32", 16), ("bf16", 32), ("bf16", 16)]
 
 
