@@ -43,6 +43,10 @@ cudaError_t cache_copy(const CacheView& c, const int* src, const int* dst, int n
 cudaError_t cache_compact(const CacheView& c, void* ws, cudaStream_t st);
 size_t cache_workspace_bytes(int pages, int slots, int n);
 
+// The partial results begin on such a boundary: the widest store of them (32 bytes, paged_tc.cu)
+// needs it. A workspace need not, so its size has room for the step up from kWorkspaceAlign.
+constexpr int kPartialAlign = 32, kWorkspaceAlign = 16;
+
 // One phase of an attention call: `items` row tiles (of up to `rows` packed
 // query rows that share a KV head), each over its own key tiles, cut
 // into even ranges for `n` streams (paged_sched.cuh).

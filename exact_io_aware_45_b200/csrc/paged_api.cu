@@ -205,6 +205,12 @@ size_t phase_bytes(const Phase& p, int d, size_t* lse_at) {
   return *lse_at + align256(rows * 4);
 }
 
+// Where the partial results begin in a workspace.
+char* partials_at(void* ws) {
+  return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + kPartialAlign - 1) &
+                                 ~uintptr_t(kPartialAlign - 1));
+}
+
 fa_status check_fwd(const CacheView& v, int B, int T, int Hq, int shared) {
   if (B < 0 || T < 0 || Hq <= 0 || Hq % v.Hkv != 0 || shared < 0) return FA_ERR_INVALID_ARG;
   if (shared & ((1 << v.page_log2) - 1)) return FA_ERR_INVALID_ARG;
@@ -255,8 +261,9 @@ fa_status fwd(const fa_cache* cache, int layer, const void* Q, void* O, float* L
   if (!plan(a, sm_count())) return FA_ERR_UNSUPPORTED;
   size_t own_lse, pre_lse;
   const size_t own = phase_bytes(a.own, v.d, &own_lse), pre = phase_bytes(a.pre, v.d, &pre_lse);
-  if (!ws || !aligned(ws, 16) || ws_bytes < own + pre) return FA_ERR_INVALID_ARG;
-  char* w = static_cast<char*>(ws);
+  if (!ws || !aligned(ws, kWorkspaceAlign)) return FA_ERR_INVALID_ARG;
+  char* const w = partials_at(ws);
+  if (ws_bytes < own + pre + (w - static_cast<char*>(ws))) return FA_ERR_INVALID_ARG;
   a.own.o = reinterpret_cast<float*>(w);
   a.own.lse = reinterpret_cast<float*>(w + own_lse);
   a.pre.o = reinterpret_cast<float*>(w + own);
@@ -361,7 +368,8 @@ size_t fa_paged_workspace_size(const fa_cache* cache, int B, int T, int Hq, int 
   sizes(a, v, B, T, Hq, shared);
   if (!plan(a, sm_count())) return 0;
   size_t at;
-  return phase_bytes(a.own, v.d, &at) + phase_bytes(a.pre, v.d, &at);
+  return phase_bytes(a.own, v.d, &at) + phase_bytes(a.pre, v.d, &at) + kPartialAlign -
+         kWorkspaceAlign;
 }
 
 fa_status fa_fwd_paged(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,

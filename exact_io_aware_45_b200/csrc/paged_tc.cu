@@ -89,7 +89,8 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// 32 bytes of registers to global memory.
+// 32 bytes of registers to global memory, on a 32-byte boundary.
+static_assert(kPartialAlign % 32 == 0, "partial results go out with store32");
 __device__ __forceinline__ void store32(float* to, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]),
                "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])

@@ -1,0 +1,54 @@
+"""Calls of the paged cache and its attention at the edges of what include/fa.h allows: empty
+calls, workspaces and strides of every legal kind, values that are not finite, large caps, error
+words with several bits, arguments that do not fit an int. Bounds as in test_paged.py."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+from exact_io_aware_45_b200 import fa
+from oracle import paged as orc
+from test_paged import G, TYPES, U, build, check, fwd, ints, view
+
+
+# ------------------------------------------------------------------ workspaces
+
+def cache_of(dtype, d):
+    return view(dtype=fa.FA_BF16 if dtype == "bf16" else fa.FA_F32, d=d, page_stride=2 * 16 * d)
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("T,shared", [(1, 0), (1, 32), (40, 0), (300, 64)])
+def test_workspace_has_room_for_its_own_alignment(dtype, d, T, shared):
+    """The partial results are whole multiples of 256 bytes and begin on a 32-byte boundary; a
+    workspace is 16-byte aligned, so its size has 16 bytes more."""
+    c = ctypes.byref(cache_of(dtype, d))
+    size = fa.fa_paged_workspace_size(c, 2, T, 4, shared)
+    assert size > 0 and size % 256 >= 16
+    # a workspace that begins in the middle of 32 bytes and lacks the room is refused
+    assert fwd(cache_of(dtype, d), shared or None, T=T, ws=G + 16,
+               wsb=size - 16) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("f32", 128),
+                                     ("f32", 16)])
+@pytest.mark.parametrize("B,T,Hq,shared", [(3, 1, 4, 0), (3, 40, 4, 0), (2, 150, 2, 0), (9, 20, 4, 64),
+                                           (5, 1, 4, 64), (40, 4, 8, 256)])
+def test_workspaces_aligned_to_16_bytes(dtype, d, B, T, Hq, shared):
+    """Partial results of every kernel in a workspace that no larger power of two divides, with
+    nothing written outside of it."""
+    import torch
+    lens = [shared + 700 + 90 * b for b in range(B)]
+    cache, seqs, dense = build(lens, 2, d, 16, dtype, shared=shared)
+    q = torch.randn(B, Hq, T, d, device="cuda").to(cache.dtype)
+    size = fa.fa_paged_workspace_size(cache._ref, B, T, Hq, shared)
+    buf = torch.full((size + 1024,), 0xa5, dtype=torch.uint8, device="cuda")
+    at = -buf.data_ptr() % 256 + 16
+    kw = dict(workspace=buf[at:at + size])
+    o, lse = (fa.forward_shared(q, cache, 0, shared, seqs, **kw) if shared else
+              fa.forward_paged(q, cache, 0, seqs, **kw))
+    cache.check()
+    check(o, lse, q, dense, lens, 0, dtype, 1 / math.sqrt(d))
+    assert (buf[:at] == 0xa5).all() and (buf[at + size:] == 0xa5).all()
