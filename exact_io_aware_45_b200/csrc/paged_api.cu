@@ -119,6 +119,7 @@ Family pre_family(const PagedArgs& a) {
 // packed rows each, over `keys` keys at most. It depends on sizes and types only, so the
 // workspace query and the call agree.
 Phase divide(const CacheView& v, Family kind, int groups, int rows, long long keys, int sms) {
+  if (rows < 1) rows = 1;    // an empty call launches nothing, but its workspace may be asked for
   Phase p;
   p.sms = sms;
   int per = 1;           // streams of a block

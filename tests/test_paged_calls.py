@@ -52,3 +52,33 @@ def test_workspaces_aligned_to_16_bytes(dtype, d, B, T, Hq, shared):
     cache.check()
     check(o, lse, q, dense, lens, 0, dtype, 1 / math.sqrt(d))
     assert (buf[:at] == 0xa5).all() and (buf[at + size:] == 0xa5).all()
+
+
+# ------------------------------------------------------------------ empty calls
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("B,T,shared", [(2, 0, 0), (2, 0, 16), (0, 1, 0), (0, 1, 16), (0, 40, 16),
+                                        (0, 0, 0), (0, 0, 16)])
+def test_empty_calls_have_a_workspace(dtype, d, B, T, shared):
+    c = cache_of(dtype, d)
+    assert fa.fa_paged_workspace_size(ctypes.byref(c), B, T, 4, shared) > 0
+    assert fwd(c, shared or None, B=B, T=T, Q=0) == fa.FA_OK
+    assert fa.fa_last_launch_count() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_empty_calls_in_python(dtype, d):
+    import torch
+    cache, seqs, _ = build([20, 30], 2, d, 16, dtype)
+    for B, T in ((0, 1), (2, 0), (0, 0), (0, 5)):
+        q = torch.zeros(B, 4, T, d, dtype=cache.dtype, device="cuda")
+        for o, lse in (fa.forward_paged(q, cache, 0, seqs[:B]),
+                       fa.forward_shared(q, cache, 0, 16, seqs[:B])):
+            assert o.shape == q.shape and lse.shape == (B, 4, T)
+    none = seqs[:0]
+    assert cache.extend(none, 3).numel() == 0
+    cache.fork(none, none), cache.free(none), cache.copy_pages(none, none)
+    new = torch.zeros(0, 2, d, dtype=cache.dtype, device="cuda")
+    cache.write(0, new, new, none, none)
+    cache.check()
