@@ -75,11 +75,12 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
 }
 
 // tanh(u) = 1 - 2 / (1 + e^(2u)) from the MUFU base-2 exponential and a fast
-// reciprocal; absolute error about 1e-7 (u is clamped to [-20, 20], where
-// tanh is +-1 to float precision, so the exponential stays finite). Used by
-// the soft-capping score modifier.
+// reciprocal; absolute error about 1e-7 (u is cut at 20, where tanh is 1 to
+// float precision, so that the exponential stays finite; below, it goes to 0 and
+// the result to -1). NaN stays NaN: min.NaN keeps it, fminf would not. Used by the
+// soft-capping score modifier.
 __device__ __forceinline__ float tanh_ex2(float u) {
-  u = fminf(fmaxf(u, -20.f), 20.f);
+  asm("min.NaN.f32 %0, %0, 0f41A00000;" : "+f"(u));   // 20
   const float e = ex2(u * 2.8853900817779268f);   // 2 log2(e)
   return 1.f - __fdividef(2.f, 1.f + e);
 }

@@ -82,3 +82,63 @@ def test_empty_calls_in_python(dtype, d):
     new = torch.zeros(0, 2, d, dtype=cache.dtype, device="cuda")
     cache.write(0, new, new, none, none)
     cache.check()
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+NAN_CASES = [("bf16", 128), ("bf16", 64), ("bf16", 32), ("f32", 128), ("f32", 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", NAN_CASES)
+@pytest.mark.parametrize("T,shared", [(1, 0), (3, 0), (40, 0), (160, 0), (1, 256), (4, 256)])
+@pytest.mark.parametrize("cap", [0.0, 5.0, 1e4])
+def test_nan_is_not_lost(dtype, d, T, shared, cap):
+    """A NaN in a query row makes that row NaN and leaves the others as they are, to the bit (a
+    row's arithmetic is its own); a NaN in a key makes every row NaN that sees it."""
+    import torch
+    B, Hq = (12, 8) if shared else (3, 4)
+    lens = [shared + T + 200 + 60 * b for b in range(B)]
+    cache, seqs, dense = build(lens, 2, d, 16, dtype, shared=shared)
+    q = torch.randn(B, Hq, T, d, device="cuda").to(cache.dtype)
+
+    def call():
+        return (fa.forward_shared(q, cache, 0, shared, seqs, softcap=cap) if shared else
+                fa.forward_paged(q, cache, 0, seqs, softcap=cap))
+
+    o, lse = call()
+    assert o.isfinite().all() and lse.isfinite().all()
+    b, h, t = 1, Hq - 1, T // 2
+    q[b, h, t, d // 3] = math.nan
+    o2, lse2 = call()
+    assert o2[b, h, t].isnan().all() and lse2[b, h, t].isnan()
+    o2[b, h, t], lse2[b, h, t] = o[b, h, t], lse[b, h, t]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    q[b, h, t, d // 3] = 0
+    o, lse = call()
+    j = lens[b] - 1                                      # the last token of sequence b, KV head 1
+    page = int(cache.table[int(seqs[b]), j // 16])
+    cache.k[0, page, 1, j % 16, 3] = math.nan
+    o2, lse2 = call()
+    hit = (o2[b, Hq // 2:, T - 1], lse2[b, Hq // 2:, T - 1])
+    assert all(x.isnan().all() for x in hit)
+    o2[b, Hq // 2:, T - 1], lse2[b, Hq // 2:, T - 1] = (
+        o[b, Hq // 2:, T - 1], lse[b, Hq // 2:, T - 1])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    cache.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,B,causal", [(200, 1, True), (640, 1, False), (1500, 8, True)])
+def test_nan_query_of_the_dense_forward_under_a_cap(d, N, B, causal):
+    """The row is NaN in O, and in LSE what it is without a cap."""
+    import torch
+    q, k, v = (torch.randn(B, 4, N, d, device="cuda").bfloat16() for _ in range(3))
+    q[0, 1, 77, 5] = math.nan
+    _, plain = fa.forward_mod(q, k, v, fa.mods(), causal=causal)
+    o, lse = fa.forward_mod(q, k, v, fa.mods(softcap=3.0), causal=causal)
+    assert o[0, 1, 77].isnan().all()
+    assert torch.equal(lse[0, 1, 77].nan_to_num(9.0), plain[0, 1, 77].nan_to_num(9.0))
+    o[0, 1, 77], lse[0, 1, 77] = 0, 0
+    assert o.isfinite().all() and lse.isfinite().all()
