@@ -120,13 +120,14 @@ __global__ void __launch_bounds__(kThreads, fma_blocks_per_sm(D))
     auto load = [&](int t) {
       const int st = (t - pc.t0) & 1;
       constexpr int kAll = kTile * kRowVecs;
+      const unsigned seen = sched::seen_of(a, pc, t * kTile);
 #pragma unroll
       for (int i0 = 0; i0 < kAll; i0 += kThreads) {
         const int i = i0 + tid, row = i / kRowVecs, c = i % kRowVecs;
         if (kAll % kThreads && i >= kAll) break;
         const int j = t * kTile + row;
         // rows that no query sees are not read and count as zero
-        const bool in = j >= pc.lo && j < pc.hi;
+        const bool in = (seen >> row) & 1;
         const int named = row < 16 ? page0 : page1;
         const int page = (unsigned)named < (unsigned)a.c.pages ? named : 0;
         const long long off = page * a.c.page_stride + head +

@@ -162,14 +162,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
                               (long long)(j & ((1 << a.c.page_log2) - 1)) * (D * 2) + lane * 16;
         const char* k = a.K + off;
         const char* v = a.V + off;
-        const bool edge = j < pc.lo || j + 16 > pc.hi;
+        const bool edge = j < pc.lo || j + 16 > pc.hi || pc.gaps;
+        const unsigned seen = edge ? sched::seen_of(a, pc, j) : ~0u;
 #pragma unroll
         for (int i = 0; i < kGroupBytes / 512; ++i) {
           const int vec = i * 32 + lane, row = vec / kRowVecs, c = vec % kRowVecs;
           const uint32_t dst = to + g * kGroupBytes + (c >> 3) * 2048 + row * 128 +
                                (((c & 7) ^ (row & 7)) << 4);
           // rows that no query sees are not read and count as zero
-          const int bytes = edge && (j + row < pc.lo || j + row >= pc.hi) ? 0 : 16;
+          const int bytes = (seen >> row) & 1 ? 16 : 0;
           copy16(dst, k + i * 512, bytes, policy);
           copy16(dst + kStageBytes / 2, v + i * 512, bytes, policy);
         }

@@ -54,7 +54,7 @@ __device__ __forceinline__ int own_units(const PagedArgs& a, int len) {
 }
 
 // Keys [lo, hi) that any query sees of the shared prefix, from the smallest and
-// the largest length of the batch.
+// the largest length of the sequences that are not empty.
 __device__ __forceinline__ void pre_keys(const PagedArgs& a, int least, int most, int& lo,
                                          int& hi) {
   lo = 0;
@@ -106,7 +106,7 @@ __device__ __forceinline__ void pieces_of(const Phase& ph, int s, int u, const C
 // The batch as one warp sees it: units of all sequences, those before sequence
 // `b`, the smallest and the largest length, and that of b. All lanes call it.
 struct Batch {
-  int W, before, least, most, len;
+  int W, before, least, most, len;   // (least: of the sequences that are not empty)
   int lead;          // the first sequence that reaches farthest into the shared prefix
   int lane_len;      // of sequence `lane`
 };
@@ -130,7 +130,7 @@ __device__ __forceinline__ Batch scan_batch(const PagedArgs& a, int b) {
       t.W += u;
       if (i < b) t.before += u;
       if (i == b) t.len = len[k];
-      t.least = min(t.least, len[k]);
+      if (len[k] > 0) t.least = min(t.least, len[k]);
       const int into = min(len[k], a.shared);
       if (into > reach) reach = into, t.lead = i;
       t.most = max(t.most, len[k]);
@@ -153,6 +153,7 @@ struct Walk {
   int item;          // (b * Hkv + h) * rt + row tile; (h * rt + row tile) in the shared phase
   int b, h, r;       // sequence (own phase), KV head, row tile
   int lo, hi;        // keys of the item
+  bool gaps;         // of which there may be some that no query sees
   int slot, len;     // of sequence b; the leading sequence's slot in the shared phase
   int slot1, len1;   // of the next sequence, and the slot after it: loaded ahead, since a
   int slot2;         // chain of loads per sequence would stall short ones
@@ -190,6 +191,9 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
   w.stream = i;
   if (pre) {
     pre_keys(a, t.least, t.most, w.lo, w.hi);
+    // windows of sequences that all reach behind the prefix lie within one another, others may
+    // leave keys between them
+    w.gaps = a.wl >= 0 && t.least < w.hi;
     w.u = units_of(a.pre, w.lo, w.hi);
     const Cuts c(a.pre, a.pre.items * w.u, t.W);
     if (i >= c.n) return false;
@@ -207,6 +211,7 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
                                    // first sequence may be padding, or shorter)
     return true;
   }
+  w.gaps = false;
   const Cuts c(a.own, t.W);
   if (i >= c.n) return false;
   const int per_b = a.c.Hkv * a.own.rt;
@@ -260,6 +265,7 @@ struct Piece {
   int table;         // slot whose table names the keys (the leading one's in the shared phase)
   int row0, rows;    // rows: (g, t) of sequence b, or (b, g, t) in the shared phase
   int lo, hi;        // keys in sight of any row
+  bool gaps;         // but for some between them (seen_of)
   int t0, t1;        // key tiles [t0, t1), counted from key 0
   int slot;          // partial slot, or -1: write the result
 };
@@ -274,6 +280,7 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, Walk& w) {
   p.table = w.slot;
   p.lo = w.lo;
   p.hi = w.hi;
+  p.gaps = w.gaps;
   p.row0 = w.r * ph.rows;
   p.rows = min(ph.rows, (pre ? a.B * a.TG : a.TG) - p.row0);
   const int from = w.x - w.s, to = min(w.u, w.end - w.s);
@@ -295,6 +302,28 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, Walk& w) {
     }
   }
   return p;
+}
+
+// Bits f .. e - 1 of a word, as far as they lie in it.
+__device__ __forceinline__ unsigned bits_of(int f, int e) {
+  f = max(f, 0), e = min(e, 32);
+  return f < e ? (~0u >> (32 - (e - f))) << f : 0u;
+}
+// Of the keys j0 .. j0 + 31 those of a piece's range that some query sees, one bit each: the others
+// may hold anything, and a V row that is not finite would spread through weights of 0. All lanes
+// call it. Between the windows of short sequences this takes a look at the batch per call.
+__device__ __forceinline__ unsigned seen_of(const PagedArgs& a, const Piece& p, int j0) {
+  unsigned m = ~0u;
+  if (p.gaps) {
+    m = 0;
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+      const int len = len_of(a, b);
+      const int lo = max(0ll, (long long)len - a.T - a.wl);
+      if (len > 0) m |= bits_of(lo - j0, min(len, a.shared) - j0);
+    }
+    m = __reduce_or_sync(~0u, m);
+  }
+  return m & bits_of(p.lo - j0, p.hi - j0);
 }
 
 // Keys [lo, hi) that a packed row sees in the phase, and its index in LSE (and,

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
       const bool in = j >= pc.lo && j < pc.hi;
       const long long off0 = offset(page0, j0), off1 = offset(page1, j0 + 16);
       find(t + kWarps);
+      const unsigned seen = sched::seen_of(a, pc, j0);  // what no row sees is not read
       float x[kLanes][kRows];
 #pragma unroll
       for (int g = 0; g < kLanes; ++g)
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
           const int i = g * kSide + side;
           const char* from = g < kLanes / 2 ? k0 + g * kSide * kRowBytes
                                             : k1 + (g - kLanes / 2) * kSide * kRowBytes;
-          if (j0 + i >= pc.lo && j0 + i < pc.hi) {
+          if ((seen >> i) & 1) {
             load_f<kVec>(reinterpret_cast<const T*>(from + c * kLanes * 16), kv[g]);
           } else {
 #pragma unroll
@@ -240,8 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
         const char* from = a.V + (i < 16 ? off0 + i * kRowBytes : off1 + (i - 16) * kRowBytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          // what no row sees is not read
-          if (mine && j0 + i + k >= pc.lo && j0 + i + k < pc.hi) {
+          if (mine && ((seen >> (i + k)) & 1)) {
             load_f<kPer>(reinterpret_cast<const T*>(from + k * kRowBytes) + lane * kPer, v[k]);
           } else {
 #pragma unroll

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // V_j follows K_j, or (one query tile, but for the last) K_{j+1}
         const int page = is_v && !kTwo && j + 1 < tiles ? page_v : page_k;
-        const bool edge = j0 < pc.lo || j0 + kN > pc.hi;
+        const bool edge = j0 < pc.lo || j0 + kN > pc.hi || pc.gaps;
         constexpr int kVecs = D / 8, kRows = 32 / kVecs;  // chunks of a row; rows of an instruction
         constexpr int kGroup = 16 / kRows;               // instructions for 16 keys
         const int c = lane % kVecs, rl = lane / kVecs;
@@ -250,11 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (long long)((j0 + g * 16) & ((1 << a.c.page_log2) - 1)) * (D * 2) +
                             lane * 16;
           const uint32_t dst = to + (c >> 3) * C::kBlock + g * 16 * 128;
+          const unsigned seen = edge ? sched::seen_of(a, pc, j0 + g * 16) : ~0u;
 #pragma unroll
           for (int i = 0; i < kGroup; ++i) {
-            const int r = i * kRows + rl, j = j0 + g * 16 + r;
+            const int r = i * kRows + rl;
             // rows that no query sees are not read and count as zero
-            const int bytes = edge && (j < pc.lo || j >= pc.hi) ? 0 : 16;
+            const int bytes = (seen >> r) & 1 ? 16 : 0;
             copy16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + i * 512, bytes);
           }
         }

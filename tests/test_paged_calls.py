@@ -142,3 +142,59 @@ def test_nan_query_of_the_dense_forward_under_a_cap(d, N, B, causal):
     assert torch.equal(lse[0, 1, 77].nan_to_num(9.0), plain[0, 1, 77].nan_to_num(9.0))
     o[0, 1, 77], lse[0, 1, 77] = 0, 0
     assert o.isfinite().all() and lse.isfinite().all()
+
+
+# ------------------------------------------------------------------ what no query sees
+
+def hide(cache, seqs, lens, shared, T, wl, value=math.nan):
+    """Overwrites the shared rows that no query of the call sees."""
+    page = cache.page_size
+    reach = [min(n, shared) for n in lens]
+    table = cache.table[int(seqs[reach.index(max(reach))])].tolist()
+    seen = np.zeros(shared, dtype=bool)
+    for n in lens:
+        if n:
+            seen[max(0, n - T - wl):min(n, shared)] = True
+    for j in np.flatnonzero(~seen):
+        if table[j // page] >= 0:
+            cache.k[:, table[j // page], :, j % page] = value
+            cache.v[:, table[j // page], :, j % page] = value
+    return int((~seen).sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 16), ("f32", 128),
+                                     ("f32", 64), ("f32", 16)])
+@pytest.mark.parametrize("lens,Hq,T", [
+    ([1024], 2, 1), ([1030, 0], 4, 1), ([0, 1030, 1100, 0], 8, 3),      # padding
+    ([1040, 100], 4, 1), ([100, 417, 1040, 0], 8, 2),                   # holes between windows
+    ([7, 0, 300, 555, 1024, 1025, 1200] * 5, 8, 2),
+    ([90, 400, 0], 4, 2), ([500, 130, 131] * 20, 8, 3)])                # none behind the prefix
+@pytest.mark.parametrize("wl,cap", [(0, 0.0), (37, 0.0), (200, 9.0)])
+def test_shared_rows_that_no_query_sees(dtype, d, lens, Hq, T, wl, cap):
+    """Padding and short sequences behind a prefix under a window: the rows that no query sees hold
+    NaN, before the windows and between them."""
+    import torch
+    shared = 1024
+    cache, seqs, dense = build(lens, 2, d, 32, dtype, shared=shared)
+    assert hide(cache, seqs, lens, shared, T, wl) > 0
+    q = torch.randn(len(lens), Hq, T, d, device="cuda").to(cache.dtype)
+    o, lse = fa.forward_shared(q, cache, 0, shared, seqs, window_left=wl, softcap=cap)
+    cache.check()
+    check(o, lse, q, dense, lens, 0, dtype, 1 / math.sqrt(d), wl=wl, cap=cap)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,reps", [("bf16", 128, 1), ("bf16", 64, 9), ("f32", 64, 1),
+                                          ("f32", 32, 9)])
+def test_shared_window_with_padding_out_of_range(dtype, d, reps):
+    import torch
+    lens = [300, 512, 700] * reps
+    cache, seqs, dense = build(lens, 2, d, 32, dtype, shared=256)
+    assert hide(cache, seqs, lens, 256, 1, 40) > 0
+    slots = torch.cat([ints([-1]), seqs, ints([10 ** 6])])
+    q = torch.randn(len(slots), 8, 1, d, device="cuda").to(cache.dtype)
+    o, lse = fa.forward_shared(q, cache, 0, 256, slots, window_left=40)
+    cache.check()
+    check(o[1:-1], lse[1:-1], q[1:-1], dense, lens, 0, dtype, d ** -0.5, wl=40)
+    assert not o[[0, -1]].any() and torch.isneginf(lse[[0, -1]]).all()
