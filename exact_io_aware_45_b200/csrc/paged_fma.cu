@@ -87,7 +87,9 @@ __device__ __forceinline__ void copy16(void* dst, const char* src, int bytes) {
                : "memory");
 }
 
-template <typename T, int D>
+// kGaps: a shared phase under a window, where rows that no query sees may lie between others
+// (sched::seen_of). A test of it at run time cost the other calls up to 5 %.
+template <typename T, int D, bool kGaps>
 __global__ void __launch_bounds__(kThreads, fma_blocks_per_sm(D))
     fma_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
   using Shared = FmaShared<T, D>;
@@ -120,14 +122,15 @@ __global__ void __launch_bounds__(kThreads, fma_blocks_per_sm(D))
     auto load = [&](int t) {
       const int st = (t - pc.t0) & 1;
       constexpr int kAll = kTile * kRowVecs;
-      const unsigned seen = sched::seen_of(a, pc, t * kTile);
+      unsigned seen = ~0u;
+      if constexpr (kGaps) seen = sched::seen_of(a, pc, t * kTile);
 #pragma unroll
       for (int i0 = 0; i0 < kAll; i0 += kThreads) {
         const int i = i0 + tid, row = i / kRowVecs, c = i % kRowVecs;
         if (kAll % kThreads && i >= kAll) break;
         const int j = t * kTile + row;
         // rows that no query sees are not read and count as zero
-        const bool in = (seen >> row) & 1;
+        const bool in = j >= pc.lo && j < pc.hi && (!kGaps || (seen >> row) & 1);
         const int named = row < 16 ? page0 : page1;
         const int page = (unsigned)named < (unsigned)a.c.pages ? named : 0;
         const long long off = page * a.c.page_stride + head +
@@ -269,14 +272,20 @@ __global__ void __launch_bounds__(kThreads, fma_blocks_per_sm(D))
   chain_end();
 }
 
-template <typename T, int D>
-cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
+template <typename T, int D, bool kGaps>
+cudaError_t launch_gaps(const PagedArgs& a, bool pre, cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(FmaShared<T, D>);
   static_assert((kSmem + 1024) * fma_blocks_per_sm(D) <= 228 * 1024, "shared memory of an SM");
-  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(fma_kernel<T, D>), kSmem))
-    return e;
-  return launch_chained(fma_kernel<T, D>, (pre ? a.pre : a.own).n, kThreads, kSmem, st,
-                        !pre && a.shared, a, pre);
+  const auto kernel = fma_kernel<T, D, kGaps>;
+  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmem)) return e;
+  return launch_chained(kernel, (pre ? a.pre : a.own).n, kThreads, kSmem, st, !pre && a.shared, a,
+                        pre);
+}
+
+template <typename T, int D>
+cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
+  return pre && a.wl >= 0 ? launch_gaps<T, D, true>(a, pre, st)
+                          : launch_gaps<T, D, false>(a, pre, st);
 }
 
 template <typename T>

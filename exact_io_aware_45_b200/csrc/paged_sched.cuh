@@ -311,7 +311,7 @@ __device__ __forceinline__ unsigned bits_of(int f, int e) {
 }
 // Of the keys j0 .. j0 + 31 those of a piece's range that some query sees, one bit each: the others
 // may hold anything, and a V row that is not finite would spread through weights of 0. All lanes
-// call it. Between the windows of short sequences this takes a look at the batch per call.
+// call it. Where there may be gaps it goes through the batch once.
 __device__ __forceinline__ unsigned seen_of(const PagedArgs& a, const Piece& p, int j0) {
   unsigned m = ~0u;
   if (p.gaps) {

@@ -79,7 +79,9 @@ struct SimtShared {
   int out[kRows];
 };
 
-template <typename T, int D, int kRows>
+// kGaps: a shared phase under a window, where rows that no query sees may lie between others
+// (sched::seen_of). A test of it at run time cost the other calls 2 to 17 %.
+template <typename T, int D, int kRows, bool kGaps>
 __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
     simt_kernel(const __grid_constant__ PagedArgs a, const bool pre) {
   __shared__ SimtShared<D, kRows> s;
@@ -162,7 +164,8 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
       const bool in = j >= pc.lo && j < pc.hi;
       const long long off0 = offset(page0, j0), off1 = offset(page1, j0 + 16);
       find(t + kWarps);
-      const unsigned seen = sched::seen_of(a, pc, j0);  // what no row sees is not read
+      unsigned seen = ~0u;
+      if constexpr (kGaps) seen = sched::seen_of(a, pc, j0);
       float x[kLanes][kRows];
 #pragma unroll
       for (int g = 0; g < kLanes; ++g)
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
           const int i = g * kSide + side;
           const char* from = g < kLanes / 2 ? k0 + g * kSide * kRowBytes
                                             : k1 + (g - kLanes / 2) * kSide * kRowBytes;
-          if ((seen >> i) & 1) {
+          if (j0 + i >= pc.lo && j0 + i < pc.hi) {
             load_f<kVec>(reinterpret_cast<const T*>(from + c * kLanes * 16), kv[g]);
           } else {
 #pragma unroll
@@ -241,7 +244,9 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
         const char* from = a.V + (i < 16 ? off0 + i * kRowBytes : off1 + (i - 16) * kRowBytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (mine && ((seen >> (i + k)) & 1)) {
+          // what no row sees is not read
+          if (mine && j0 + i + k >= pc.lo && j0 + i + k < pc.hi &&
+              (!kGaps || (seen >> (i + k)) & 1)) {
             load_f<kPer>(reinterpret_cast<const T*>(from + k * kRowBytes) + lane * kPer, v[k]);
           } else {
 #pragma unroll
@@ -298,12 +303,19 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
   chain_end();
 }
 
+template <typename T, int D, bool kGaps>
+cudaError_t launch_simt_rows(const PagedArgs& a, bool pre, cudaStream_t st) {
+  const Phase& ph = pre ? a.pre : a.own;
+  const auto kernel = ph.rows == 1   ? simt_kernel<T, D, 1, kGaps>
+                      : ph.rows == 2 ? simt_kernel<T, D, 2, kGaps>
+                                     : simt_kernel<T, D, 4, kGaps>;
+  return launch_chained(kernel, ph.n, kWarps * 32, 0, st, !pre && a.shared, a, pre);
+}
+
 template <typename T, int D>
 cudaError_t launch_simt(const PagedArgs& a, bool pre, cudaStream_t st) {
-  const Phase& ph = pre ? a.pre : a.own;
-  const auto kernel = ph.rows == 1 ? simt_kernel<T, D, 1> : ph.rows == 2 ? simt_kernel<T, D, 2>
-                                                                         : simt_kernel<T, D, 4>;
-  return launch_chained(kernel, ph.n, kWarps * 32, 0, st, !pre && a.shared, a, pre);
+  return pre && a.wl >= 0 ? launch_simt_rows<T, D, true>(a, pre, st)
+                          : launch_simt_rows<T, D, false>(a, pre, st);
 }
 
 template <typename T>
