@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, fma_blocks_per_sm(D))
       const int st = (t - pc.t0) & 1;
       constexpr int kAll = kTile * kRowVecs;
       unsigned seen = ~0u;
-      if constexpr (kGaps) seen = sched::seen_of(a, pc, t * kTile);
+      if constexpr (kGaps) seen = sched::seen_of(a, pc, t * kTile, pc.len);
 #pragma unroll
       for (int i0 = 0; i0 < kAll; i0 += kThreads) {
         const int i = i0 + tid, row = i / kRowVecs, c = i % kRowVecs;

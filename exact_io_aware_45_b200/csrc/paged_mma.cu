@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
                pc.hi > pc.lo ? (pc.hi - 1) >> a.c.page_log2 : -1);
     const long long head = (long long)pc.h * a.c.head_bytes;
 
+    const bool gaps = pre && pc.len;
+
     // tile t into its stage: 16 keys of one head and page are 16 * d contiguous elements
     auto load = [&](int t) {
       const uint32_t to = ring + (uint32_t)(t - pc.t0) % kStages * kStageBytes;
@@ -162,8 +164,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
                               (long long)(j & ((1 << a.c.page_log2) - 1)) * (D * 2) + lane * 16;
         const char* k = a.K + off;
         const char* v = a.V + off;
-        const bool edge = j < pc.lo || j + 16 > pc.hi || pc.gaps;
-        const unsigned seen = edge ? sched::seen_of(a, pc, j) : ~0u;
+        const bool edge = j < pc.lo || j + 16 > pc.hi || gaps;
+        const unsigned seen = edge ? sched::seen_of(a, pc, j, gaps) : ~0u;
 #pragma unroll
         for (int i = 0; i < kGroupBytes / 512; ++i) {
           const int vec = i * 32 + lane, row = vec / kRowVecs, c = vec % kRowVecs;

@@ -153,8 +153,8 @@ struct Walk {
   int item;          // (b * Hkv + h) * rt + row tile; (h * rt + row tile) in the shared phase
   int b, h, r;       // sequence (own phase), KV head, row tile
   int lo, hi;        // keys of the item
-  bool gaps;         // of which there may be some that no query sees
-  int slot, len;     // of sequence b; the leading sequence's slot in the shared phase
+  int slot, len;     // of sequence b; the leading sequence's slot in the shared phase, where len
+                     // says whether there may be keys in [lo, hi) that no query sees
   int slot1, len1;   // of the next sequence, and the slot after it: loaded ahead, since a
   int slot2;         // chain of loads per sequence would stall short ones
 };
@@ -193,7 +193,7 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
     pre_keys(a, t.least, t.most, w.lo, w.hi);
     // windows of sequences that all reach behind the prefix lie within one another, others may
     // leave keys between them
-    w.gaps = a.wl >= 0 && t.least < w.hi;
+    w.len = a.wl >= 0 && t.least < w.hi;
     w.u = units_of(a.pre, w.lo, w.hi);
     const Cuts c(a.pre, a.pre.items * w.u, t.W);
     if (i >= c.n) return false;
@@ -206,12 +206,11 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
     w.s = w.item * w.u;
     w.h = w.item / a.pre.rt;
     w.r = w.item - w.h * a.pre.rt;
-    w.b = w.len = 0;
+    w.b = 0;
     w.slot = slot_of(a, t.lead);   // its table names all of the prefix that is in sight (the
                                    // first sequence may be padding, or shorter)
     return true;
   }
-  w.gaps = false;
   const Cuts c(a.own, t.W);
   if (i >= c.n) return false;
   const int per_b = a.c.Hkv * a.own.rt;
@@ -261,11 +260,10 @@ __device__ inline bool begin(const PagedArgs& a, bool pre, int i, Walk& w) {
 // One piece of an item.
 struct Piece {
   int h;             // KV head
-  int b, len;        // sequence and its length (own phase)
+  int b, len;        // sequence and its length (own phase), or whether there may be gaps (shared)
   int table;         // slot whose table names the keys (the leading one's in the shared phase)
   int row0, rows;    // rows: (g, t) of sequence b, or (b, g, t) in the shared phase
   int lo, hi;        // keys in sight of any row
-  bool gaps;         // but for some between them (seen_of)
   int t0, t1;        // key tiles [t0, t1), counted from key 0
   int slot;          // partial slot, or -1: write the result
 };
@@ -280,7 +278,6 @@ __device__ __forceinline__ Piece next(const PagedArgs& a, bool pre, Walk& w) {
   p.table = w.slot;
   p.lo = w.lo;
   p.hi = w.hi;
-  p.gaps = w.gaps;
   p.row0 = w.r * ph.rows;
   p.rows = min(ph.rows, (pre ? a.B * a.TG : a.TG) - p.row0);
   const int from = w.x - w.s, to = min(w.u, w.end - w.s);
@@ -312,9 +309,10 @@ __device__ __forceinline__ unsigned bits_of(int f, int e) {
 // Of the keys j0 .. j0 + 31 those of a piece's range that some query sees, one bit each: the others
 // may hold anything, and a V row that is not finite would spread through weights of 0. All lanes
 // call it. Where there may be gaps it goes through the batch once.
-__device__ __forceinline__ unsigned seen_of(const PagedArgs& a, const Piece& p, int j0) {
+__device__ __forceinline__ unsigned seen_of(const PagedArgs& a, const Piece& p, int j0,
+                                            bool gaps) {
   unsigned m = ~0u;
-  if (p.gaps) {
+  if (gaps) {
     m = 0;
     for (int b = threadIdx.x & 31; b < a.B; b += 32) {
       const int len = len_of(a, b);

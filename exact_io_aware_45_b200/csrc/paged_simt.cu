@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_blocks_per_sm(D, kRows))
       const long long off0 = offset(page0, j0), off1 = offset(page1, j0 + 16);
       find(t + kWarps);
       unsigned seen = ~0u;
-      if constexpr (kGaps) seen = sched::seen_of(a, pc, j0);
+      if constexpr (kGaps) seen = sched::seen_of(a, pc, j0, pc.len);
       float x[kLanes][kRows];
 #pragma unroll
       for (int g = 0; g < kLanes; ++g)

@@ -100,7 +100,9 @@ __device__ __forceinline__ void copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int D, bool kTwo>
+// kGaps: a shared phase under a window, where rows that no query sees may lie between others
+// (sched::seen_of).
+template <int D, bool kTwo, bool kGaps>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_kernel(const __grid_constant__ PagedArgs a, const bool pre, const long long stall) {
   using C = Cfg<D, kTwo>;
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // V_j follows K_j, or (one query tile, but for the last) K_{j+1}
         const int page = is_v && !kTwo && j + 1 < tiles ? page_v : page_k;
-        const bool edge = j0 < pc.lo || j0 + kN > pc.hi || pc.gaps;
+        const bool edge = j0 < pc.lo || j0 + kN > pc.hi;
         constexpr int kVecs = D / 8, kRows = 32 / kVecs;  // chunks of a row; rows of an instruction
         constexpr int kGroup = 16 / kRows;               // instructions for 16 keys
         const int c = lane % kVecs, rl = lane / kVecs;
@@ -250,12 +252,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (long long)((j0 + g * 16) & ((1 << a.c.page_log2) - 1)) * (D * 2) +
                             lane * 16;
           const uint32_t dst = to + (c >> 3) * C::kBlock + g * 16 * 128;
-          const unsigned seen = edge ? sched::seen_of(a, pc, j0 + g * 16) : ~0u;
+          unsigned seen = ~0u;
+          if constexpr (kGaps) seen = sched::seen_of(a, pc, j0 + g * 16, pc.len);
 #pragma unroll
           for (int i = 0; i < kGroup; ++i) {
-            const int r = i * kRows + rl;
+            const int r = i * kRows + rl, j = j0 + g * 16 + r;
             // rows that no query sees are not read and count as zero
-            const int bytes = (seen >> r) & 1 ? 16 : 0;
+            const bool out = edge && (j < pc.lo || j >= pc.hi);
+            const int bytes = out || (kGaps && !((seen >> r) & 1)) ? 0 : 16;
             copy16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + i * 512, bytes);
           }
         }
@@ -568,15 +572,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   chain_end();
 }
 
-template <int D, bool kTwo>
-cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
+template <int D, bool kTwo, bool kGaps>
+cudaError_t launch_gaps(const PagedArgs& a, bool pre, cudaStream_t st) {
   using C = Cfg<D, kTwo>;
   static_assert(C::kBytes + sizeof(Control) <= 227 * 1024, "shared memory");
-  if (cudaError_t e =
-          set_max_dynamic_smem(reinterpret_cast<const void*>(tc_kernel<D, kTwo>), C::kBytes))
+  const auto kernel = tc_kernel<D, kTwo, kGaps>;
+  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), C::kBytes))
     return e;
-  return launch_chained(tc_kernel<D, kTwo>, (pre ? a.pre : a.own).n, kThreads, C::kBytes, st,
+  return launch_chained(kernel, (pre ? a.pre : a.own).n, kThreads, C::kBytes, st,
                         !pre && a.shared, a, pre, debug_stall_cycles(kStallFwd));
+}
+
+template <int D, bool kTwo>
+cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
+  return pre && a.wl >= 0 ? launch_gaps<D, kTwo, true>(a, pre, st)
+                          : launch_gaps<D, kTwo, false>(a, pre, st);
 }
 
 }  // namespace
