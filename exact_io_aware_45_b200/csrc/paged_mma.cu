@@ -241,8 +241,12 @@ __global__ void __launch_bounds__(kMmaWarps * 32, kMmaBlocksPerSm)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float z = x[g][n][i] + y[g][n][i];
-              if (a.softcap > 0.f) z = cap2 * tanh_ex2(z * to_cap);
-              else z *= scale2;
+              if (a.softcap > kWideCap)
+                z = kLog2e * soft_cap(z * a.scale, a.softcap, cap_inverse(a.softcap));
+              else if (a.softcap > 0.f)
+                z = cap2 * tanh_ex2(z * to_cap);
+              else
+                z *= scale2;
               x[g][n][i] = z;
             }
         if (j0 < lo_all || j0 + kTile > hi_all) {

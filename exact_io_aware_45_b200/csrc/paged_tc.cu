@@ -100,9 +100,10 @@ __device__ __forceinline__ void copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// kGaps: a shared phase under a window, where rows that no query sees may lie between others
-// (sched::seen_of).
-template <int D, bool kTwo, bool kGaps>
+// kRare: a shared phase under a window, where rows that no query sees may lie between others
+// (sched::seen_of), or a wide soft cap (soft_cap). Code for them in the usual kernel, never run,
+// costs it up to 4 %.
+template <int D, bool kTwo, bool kRare>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_kernel(const __grid_constant__ PagedArgs a, const bool pre, const long long stall) {
   using C = Cfg<D, kTwo>;
@@ -253,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             lane * 16;
           const uint32_t dst = to + (c >> 3) * C::kBlock + g * 16 * 128;
           unsigned seen = ~0u;
-          if constexpr (kGaps) seen = sched::seen_of(a, pc, j0 + g * 16, pc.len);
+          if constexpr (kRare) seen = sched::seen_of(a, pc, j0 + g * 16, pre && pc.len);
 #pragma unroll
           for (int i = 0; i < kGroup; ++i) {
             const int r = i * kRows + rl, j = j0 + g * 16 + r;
             // rows that no query sees are not read and count as zero
             const bool out = edge && (j < pc.lo || j >= pc.hi);
-            const int bytes = out || (kGaps && !((seen >> r) & 1)) ? 0 : 16;
+            const int bytes = out || (kRare && !((seen >> r) & 1)) ? 0 : 16;
             copy16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + i * 512, bytes);
           }
         }
@@ -384,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_reg = tm + C::kO + t * D + lanes;
     const bool xform = a.softcap > 0.f || a.scale <= 0.f;
     const float scale2 = a.scale * kLog2e;
-    const float c = xform ? 1.f : scale2;
+    const bool wide = kRare && a.softcap > kWideCap;
+    const float c = wide ? kLog2e : xform ? 1.f : scale2;
     const float cap2 = a.softcap * kLog2e;
     const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
     uint32_t cnt = 0;                                    // this warpgroup's tiles so far
@@ -405,7 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x[128];
         tmem_ld128(s_reg, x);
         if (xform) {
-          if (a.softcap > 0.f) {
+          if (wide) {
+            const float inv = cap_inverse(a.softcap);
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              x[i] = __float_as_uint(soft_cap(__uint_as_float(x[i]) * a.scale, a.softcap, inv));
+          } else if (a.softcap > 0.f) {
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               x[i] = __float_as_uint(cap2 * tanh_ex2(__uint_as_float(x[i]) * to_cap));
@@ -572,11 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   chain_end();
 }
 
-template <int D, bool kTwo, bool kGaps>
-cudaError_t launch_gaps(const PagedArgs& a, bool pre, cudaStream_t st) {
+template <int D, bool kTwo, bool kRare>
+cudaError_t launch_as(const PagedArgs& a, bool pre, cudaStream_t st) {
   using C = Cfg<D, kTwo>;
   static_assert(C::kBytes + sizeof(Control) <= 227 * 1024, "shared memory");
-  const auto kernel = tc_kernel<D, kTwo, kGaps>;
+  const auto kernel = tc_kernel<D, kTwo, kRare>;
   if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), C::kBytes))
     return e;
   return launch_chained(kernel, (pre ? a.pre : a.own).n, kThreads, C::kBytes, st,
@@ -585,8 +592,8 @@ cudaError_t launch_gaps(const PagedArgs& a, bool pre, cudaStream_t st) {
 
 template <int D, bool kTwo>
 cudaError_t launch(const PagedArgs& a, bool pre, cudaStream_t st) {
-  return pre && a.wl >= 0 ? launch_gaps<D, kTwo, true>(a, pre, st)
-                          : launch_gaps<D, kTwo, false>(a, pre, st);
+  return (pre && a.wl >= 0) || a.softcap > kWideCap ? launch_as<D, kTwo, true>(a, pre, st)
+                                                    : launch_as<D, kTwo, false>(a, pre, st);
 }
 
 }  // namespace

@@ -466,7 +466,8 @@ fa_status fa_cache_compact(const fa_cache* cache, void* workspace, size_t worksp
  * sequence in slot seqs[b] (slot b when seqs == NULL) has position
  * i = len - T + t and sees key j < len iff
  *   (causal == 0 or j <= i) and (window_left < 0 or j >= i - window_left);
- * softcap > 0 caps the scores as in fa_mods. A query that sees no key (an
+ * softcap > 0 caps the scores as in fa_mods; a capped score is off by no more than
+ * 4e-7 of the cap (caps up to 64) or 2e-6 of its own value. A query that sees no key (an
  * empty slot, i < 0, seqs[b] out of range) gets O = 0 and LSE = -inf. K and V
  * rows that no query of the call sees may hold anything. A non-finite V row that
  * one query sees may spread to the call's other queries of that KV head. Table

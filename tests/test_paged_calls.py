@@ -198,3 +198,42 @@ def test_shared_window_with_padding_out_of_range(dtype, d, reps):
     cache.check()
     check(o[1:-1], lse[1:-1], q[1:-1], dense, lens, 0, dtype, d ** -0.5, wl=40)
     assert not o[[0, -1]].any() and torch.isneginf(lse[[0, -1]]).all()
+
+
+# ------------------------------------------------------------------ large caps
+
+def check_cap(o, lse, q, dense, lens, dtype, scale, cap):
+    """As check, but the cap costs a score at most 2^-19 of its own size: tanh off by 1.5e-6 of its
+    value, products by three roundings."""
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    T, d = o.shape[2:]
+    for b, n in enumerate(lens):
+        k, v = (x[0].float().cpu().numpy() for x in dense[b])
+        O, L, A, X = orc.attend(q[b].float().cpu().numpy(), k, v, T, n - T, scale, softcap=cap)
+        dx = (2 * (d + 8) * U + 2.0 ** -19) * X
+        tol = A * (2 * dx + 2 * (n + 64) * U + 2.0 ** -20)[..., None]
+        if dtype == "bf16":
+            tol = tol + 2.0 ** -8 * (A + np.abs(O))
+        off = (np.abs(o[b] - O) - tol).max()
+        assert off <= 0, f"sequence {b}: O off by {off:.3e} too much"
+        off = (np.abs(lse[b] - L) - dx - (n + 64) * U - 2.0 ** -20 * (1 + np.abs(L))).max()
+        assert off <= 0, f"sequence {b}: LSE off by {off:.3e} too much"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("B,T,shared", [(3, 1, 0), (3, 5, 0), (3, 40, 0), (2, 150, 0), (20, 4, 256)])
+@pytest.mark.parametrize("cap", [0.05, 1e3, 1e6, 3e38])
+@pytest.mark.parametrize("scale", [None, -1e-3])
+def test_caps_of_every_size(dtype, d, B, T, shared, cap, scale):
+    """A cap far above the scores changes them by less than their rounding."""
+    import torch
+    lens = [shared + T + 80 + 37 * b for b in range(B)]
+    cache, seqs, dense = build(lens, 2, d, 16, dtype, shared=shared)
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    q = torch.randn(B, 8, T, d, device="cuda").to(cache.dtype)
+    kw = dict(scale=scale, softcap=cap)
+    o, lse = (fa.forward_shared(q, cache, 0, shared, seqs, **kw) if shared else
+              fa.forward_paged(q, cache, 0, seqs, **kw))
+    cache.check()
+    check_cap(o, lse, q, dense, lens, dtype, scale, cap)
