@@ -237,3 +237,45 @@ def test_caps_of_every_size(dtype, d, B, T, shared, cap, scale):
               fa.forward_paged(q, cache, 0, seqs, **kw))
     cache.check()
     check_cap(o, lse, q, dense, lens, dtype, scale, cap)
+
+
+# ------------------------------------------------------------------ one workspace, many calls
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("T,shared", [(1, 0), (40, 0), (1, 512), (6, 512)])
+def test_calls_that_follow_on_one_workspace(dtype, d, T, shared):
+    """Two queries in turn on one workspace, back to back and captured: each result is its own,
+    none is joined from what the call before left there."""
+    import torch
+    lens = [shared + 900 + 50 * b for b in range(7)]
+    cache, seqs, dense = build(lens, 2, d, 16, dtype, shared=shared)
+    qs = [torch.randn(7, 8, T, d, device="cuda").to(cache.dtype) for _ in range(2)]
+    ws = torch.empty(fa.fa_paged_workspace_size(cache._ref, 7, T, 8, shared), dtype=torch.uint8,
+                     device="cuda")
+
+    def call(q, **kw):
+        return (fa.forward_shared(q, cache, 0, shared, seqs, **kw) if shared else
+                fa.forward_paged(q, cache, 0, seqs, **kw))
+
+    want = [call(q) for q in qs]
+    for q, w in zip(qs, want):
+        check(*w, q, dense, lens, 0, dtype, 1 / math.sqrt(d))
+    n = 60
+    got = [[torch.empty_like(x) for x in want[0]] for _ in range(n)]
+
+    def run():
+        for i, (o, lse) in enumerate(got):
+            call(qs[i % 2], out=o, lse=lse, workspace=ws)
+
+    run()
+    first = [[x.clone() for x in g] for g in got]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for i in range(n):
+        for x, y, w in zip(first[i], got[i], want[i % 2]):
+            assert torch.equal(x, w) and torch.equal(y, w)
