@@ -482,7 +482,11 @@ fa_status fa_get_device_error(void* workspace, void* stream) {
     return FA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
   if (word == 0) return FA_OK;
-  if (cudaMemsetAsync(workspace, 0, sizeof(word), st) != cudaSuccess) return FA_ERR_CUDA;
+  // a refused cache call stays for the next read when a timeout is reported
+  const unsigned rest = (word & kErrTimeout) ? word & kErrCache : 0u;
+  if ((rest ? cudaMemcpyAsync(workspace, &rest, sizeof(rest), cudaMemcpyHostToDevice, st)
+            : cudaMemsetAsync(workspace, 0, sizeof(rest), st)) != cudaSuccess)
+    return FA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
   if (word & kErrTimeout) return FA_ERR_TIMEOUT;
   return (word & kErrCache) ? FA_ERR_CACHE : FA_ERR_CUDA;

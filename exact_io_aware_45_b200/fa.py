@@ -668,8 +668,8 @@ class PagedCache:
         self._call(self._compact, ws.data_ptr(), size)
 
     def check(self):
-        """Raises FaError if the device refused a call since the last check
-        (synchronises the stream)."""
+        """Raises FaError if the device refused a call or a wait ran out since the last
+        check (synchronises the stream); if both, the refusal is left for the next check."""
         with self._torch.cuda.device(self._index):
             _check(fa_get_device_error(_ptr(self.err), self._raw_stream(self._index)),
                    "paged cache")

@@ -508,7 +508,8 @@ int fa_last_launch_count(void);
  * the word to the host, then zeroes it. Returns FA_OK if no kernel recorded a
  * failure, FA_ERR_TIMEOUT if a bounded wait ran out, FA_ERR_CACHE if a cache
  * operation was refused (`workspace` is then the cache's err), FA_ERR_CUDA if the copy
- * failed (and then leaves the word as it is).
+ * failed (and then leaves the word as it is). A word that holds both a timeout and a
+ * refusal gives FA_ERR_TIMEOUT and keeps the refusal for the next call.
  */
 fa_status fa_get_device_error(void* workspace, void* stream);
 

@@ -279,3 +279,47 @@ def test_calls_that_follow_on_one_workspace(dtype, d, T, shared):
     for i in range(n):
         for x, y, w in zip(first[i], got[i], want[i % 2]):
             assert torch.equal(x, w) and torch.equal(y, w)
+
+
+# ------------------------------------------------------------------ error words
+
+@pytest.mark.gpu
+def test_a_refusal_and_a_timeout_are_both_reported():
+    """A refused extension and a wait that ran out between two checks: neither hides the other."""
+    import torch
+    lens = [400, 401, 402]
+    cache, seqs, dense = build(lens, 2, 64, 16, "bf16")
+    q = torch.randn(3, 8, 30, 64, device="cuda").bfloat16()
+    fa.forward_paged(q, cache, 0, seqs)
+    torch.cuda.synchronize()
+    assert (cache.extend(ints([0, 0]), 1) == -1).all()
+    assert fa.fa_debug_set_stall(fa.FA_STALL_FWD, 4_000_000) == fa.FA_OK
+    try:
+        fa.forward_paged(q, cache, 0, seqs)
+        torch.cuda.synchronize()
+    finally:
+        fa.fa_debug_set_stall(0, 0)
+    found = []
+    for _ in range(2):
+        with pytest.raises(fa.FaError) as e:
+            cache.check()
+        found.append(e.value.status)
+    assert sorted(found) == [fa.FA_ERR_TIMEOUT, fa.FA_ERR_CACHE]
+    cache.check()
+    assert not cache.err.any()
+    o, lse = fa.forward_paged(q, cache, 0, seqs)
+    check(o, lse, q, dense, lens, 0, "bf16", 0.125)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("word,want", [(1, [fa.FA_ERR_TIMEOUT]), (2, [fa.FA_ERR_CUDA]),
+                                       (4, [fa.FA_ERR_CACHE]), (3, [fa.FA_ERR_TIMEOUT]),
+                                       (7, [fa.FA_ERR_TIMEOUT, fa.FA_ERR_CACHE])])
+def test_error_words(word, want):
+    """Each status once, and the word is clear afterwards."""
+    import torch
+    err = torch.zeros(64, dtype=torch.int32, device="cuda")
+    err[0] = word
+    for w in want + [fa.FA_OK]:
+        assert fa.fa_get_device_error(err.data_ptr(), torch.cuda.current_stream().cuda_stream) == w
+    assert not err.any()
