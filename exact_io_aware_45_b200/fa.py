@@ -532,10 +532,16 @@ class PagedCache:
 
     def __init__(self, k, v, table, lens, refs):
         import torch
-        if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+        if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v are [layers, pages, Hkv, page_size, d] of one type and stride")
         L, P, Hkv, ps, d = k.shape
-        if min(k.shape) < 1 or k.stride()[2:] != (ps * d, d, 1):
+        # the stride of a dimension of one entry moves nothing: as in a contiguous tensor
+        plain = (P * Hkv * ps * d, Hkv * ps * d, ps * d, d, 1)
+        stride, v_stride = (tuple(p if n == 1 else s for n, s, p in zip(t.shape, t.stride(), plain))
+                            for t in (k, v))
+        if stride != v_stride:
+            raise ValueError("k and v are [layers, pages, Hkv, page_size, d] of one type and stride")
+        if min(k.shape) < 1 or stride[2:] != plain[2:]:
             raise ValueError("a page [Hkv, page_size, d] of k and v is contiguous and not empty")
         if table.dim() != 2 or lens.shape != table.shape[:1] or refs.shape != (P,):
             raise ValueError("table is [seqs, seq_pages], lens [seqs], refs [pages]")
@@ -548,7 +554,7 @@ class PagedCache:
         self.device, self.dtype = k.device, k.dtype
         self.layers, self.pages, self.Hkv, self.page_size, self.d = k.shape
         self.err = torch.zeros(64, dtype=torch.int32, device=k.device)
-        self._c = FaCache(_ptr(k), _ptr(v), k.stride(0), k.stride(1), L, P, Hkv, ps, d,
+        self._c = FaCache(_ptr(k), _ptr(v), stride[0], stride[1], L, P, Hkv, ps, d,
                           _dtype_code(k.dtype), _ptr(table), _ptr(lens), _ptr(refs),
                           table.shape[0], table.shape[1], _ptr(self.err))
         # a call costs the host as much as small ones cost the GPU: what every call needs is

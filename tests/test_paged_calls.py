@@ -323,3 +323,36 @@ def test_error_words(word, want):
     for w in want + [fa.FA_OK]:
         assert fa.fa_get_device_error(err.data_ptr(), torch.cuda.current_stream().cuda_stream) == w
     assert not err.any()
+
+
+# ------------------------------------------------------------------ strides of single entries
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_of_dimensions_of_one_entry_do_not_matter(dtype):
+    """One KV head kept as [pages, page, 1, d], one layer, one page: the same bytes, other strides."""
+    import torch
+    lens = [70, 5]
+    cache, seqs, dense = build(lens, 1, 64, 16, dtype)
+    q = torch.randn(2, 4, 1, 64, device="cuda").to(cache.dtype)
+    want = fa.forward_paged(q, cache, 0, seqs)
+    rest = (cache.table, cache.lens, cache.refs)
+    P = cache.pages
+    views = [cache.k[0, :, 0].unsqueeze(2).transpose(1, 2)[None],              # [1, P, 1, 16, 64]
+             cache.k.as_strided((1, P, 1, 16, 64), (3, 1024, 7, 64, 1))]
+    for k in views:
+        for v in (cache.v, cache.v.as_strided(k.shape, (5, 1024, 1, 64, 1))):
+            o, lse = fa.forward_paged(q, fa.PagedCache(k, v, *rest), 0, seqs)
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    small = fa.PagedCache.new(1, 1, 1, 16, 64, 1, 1, cache.dtype)
+    k, v = (x.as_strided((1, 1, 1, 16, 64), (1, 1, 1, 64, 1)) for x in (small.k, small.v))
+    one = fa.PagedCache(k, v, small.table, small.lens, small.refs)
+    pos = one.extend(ints([0]), 9)
+    new = torch.randn(9, 1, 64, device="cuda").to(cache.dtype)
+    one.write(0, new, new, ints([0]), pos)
+    one.check()
+    assert torch.equal(small.k[0, 0, 0, :9], new[:, 0])
+    for stride in ((0, 1024, 0, 64, 2), (0, 1025, 0, 64, 1), (0, 1024, 0, 0, 1)):
+        bad = cache.k.as_strided((1, P - 1, 1, 16, 64), stride)
+        with pytest.raises(ValueError):
+            fa.PagedCache(bad, bad, cache.table, cache.lens, cache.refs[:-1])
