@@ -519,6 +519,16 @@ def attention(q, k, v, scale: Optional[float] = None, causal: bool = False, bloc
 
 # ------------------------------------------------------------------ paged cache
 
+_INT_MIN, _INT_MAX = -1 << 31, (1 << 31) - 1
+
+
+def _c_int(x) -> int:
+    """A number for an int argument of the library; ctypes would take it modulo 2^32."""
+    if not _INT_MIN <= x <= _INT_MAX:
+        raise ValueError(f"{x} does not fit an int")
+    return x
+
+
 class PagedCache:
     """Keys and values of many sequences in a pool of fixed-size pages (fa_cache
     of include/fa.h, which says what the calls do and when they are refused).
@@ -588,7 +598,8 @@ class PagedCache:
         if t.dtype is not self._int32 or t.dim() != 1 or not t.is_contiguous() or \
                 t.get_device() != self._index:
             raise ValueError("a list is a contiguous int32 tensor on the cache's device")
-        return t.numel()
+        n = t.numel()
+        return n if n <= _INT_MAX else _c_int(n)
 
     def _call(self, fn, *args):
         """A library call on the cache's device and its current stream."""
@@ -619,7 +630,7 @@ class PagedCache:
                 raise ValueError("cu_seqlens has one entry more than the list of sequences")
             cu, each = tokens.data_ptr(), 0
         else:
-            cu, each = 0, int(tokens)
+            cu, each = 0, _c_int(int(tokens))
         pos = seqs.new_empty(n)
         ws, size = self._workspace(n)
         self._call(self._extend, seqs.data_ptr(), n, cu, each, pos.data_ptr(),
@@ -644,8 +655,8 @@ class PagedCache:
                 raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
         if len(shape) != 3 or shape[1] != self.Hkv or shape[2] != self.d:
             raise ValueError("k and v are contiguous [total, Hkv, d] of the cache's type")
-        self._call(self._write, layer, k.data_ptr(), v.data_ptr(), seqs.data_ptr(),
-                   pos.data_ptr(), n, cu, shape[0])
+        self._call(self._write, _c_int(layer), k.data_ptr(), v.data_ptr(), seqs.data_ptr(),
+                   pos.data_ptr(), n, cu, _c_int(shape[0]))
 
     def _pairs(self, fn, src, dst):
         n = self._list(src)
@@ -688,6 +699,9 @@ def _forward_cache(q, cache, layer, shared, seqs, scale, causal, window_left, so
             len(shape) != 4 or shape[3] != cache.d:
         raise ValueError("q is a contiguous [B, Hq, T, d] of the cache's type, on its device")
     B, Hq, T, d = shape
+    if not (_INT_MIN <= layer <= _INT_MAX and _INT_MIN <= shared <= _INT_MAX and
+            _INT_MIN <= window_left <= _INT_MAX):      # (in line: a call takes the host 15 us)
+        raise ValueError("layer, shared and window_left are ints of 32 bits")
     if seqs is not None and cache._list(seqs) != B:
         raise ValueError("one sequence for each batch entry")
     torch = cache._torch

@@ -356,3 +356,25 @@ def test_strides_of_dimensions_of_one_entry_do_not_matter(dtype):
         bad = cache.k.as_strided((1, P - 1, 1, 16, 64), stride)
         with pytest.raises(ValueError):
             fa.PagedCache(bad, bad, cache.table, cache.lens, cache.refs[:-1])
+
+
+# ------------------------------------------------------------------ numbers that do not fit an int
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 31) - 1, 1 << 63, 1 << 70])
+def test_numbers_that_do_not_fit_are_refused(n):
+    """None is taken modulo 2^32."""
+    import torch
+    cache, seqs, _ = build([20, 30], 2, 64, 16, "bf16")
+    q = torch.randn(2, 4, 1, 64, device="cuda").bfloat16()
+    new = torch.zeros(2, 2, 64, device="cuda").bfloat16()
+    keep = cache.lens.clone()
+    for call in (lambda: cache.extend(seqs, n), lambda: fa.forward_paged(q, cache, n, seqs),
+                 lambda: fa.forward_paged(q, cache, 0, seqs, window_left=n),
+                 lambda: fa.forward_shared(q, cache, 0, n, seqs),
+                 lambda: fa.forward_shared(q, cache, n, 16, seqs),
+                 lambda: cache.write(n, new, new, seqs, keep[:2])):
+        with pytest.raises((ValueError, fa.FaError)):
+            call()
+    assert torch.equal(cache.lens, keep)
+    cache.check()
