@@ -269,8 +269,11 @@ __global__ void __launch_bounds__(256)
   const int row_log2 = 31 - __clz(row_vecs);
   const int vecs = c.Hkv * row_vecs;
   const int ps_mask = (1 << c.page_log2) - 1;
-  const int warps = gridDim.x * (blockDim.x >> 5);
-  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < total; r += warps) {
+  const unsigned warps = gridDim.x * (blockDim.x >> 5);
+  // (unsigned: the last step may pass 2^31)
+  for (unsigned row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); row < (unsigned)total;
+       row += warps) {
+    const int r = (int)row;
     const int4* k = reinterpret_cast<const int4*>(K + (size_t)r * c.Hkv * c.row_bytes);
     const int4* v = reinterpret_cast<const int4*>(V + (size_t)r * c.Hkv * c.row_bytes);
     int4 x[kAtOnce], y[kAtOnce];

@@ -45,7 +45,7 @@ fa_status view_of(const fa_cache* c, CacheView& v) {
   const long long page = (long long)c->Hkv * c->page_size * c->d;
   if (page * es >= (1ll << 30) || c->pages >= (1 << 28) || c->layers >= (1 << 16) ||
       (long long)c->seq_pages * c->page_size >= (1ll << 30) ||
-      (long long)c->seqs * c->seq_pages >= (1ll << 31))
+      (long long)c->seqs * c->seq_pages >= (1ll << 31) - (1 << 16))   // loops step past it
     return FA_ERR_UNSUPPORTED;
   if (c->page_stride < page || (c->layers > 1 && c->layer_stride < page))
     return FA_ERR_INVALID_ARG;

@@ -378,3 +378,31 @@ def test_numbers_that_do_not_fit_are_refused(n):
             call()
     assert torch.equal(cache.lens, keep)
     cache.check()
+
+
+# ------------------------------------------------------------------ the longest lists
+
+def test_more_slots_than_loops_can_count():
+    """Loops over slots step past their number, in 32 bits."""
+    for seqs in ((1 << 31) - 1, (1 << 31) - 4096):
+        c = ctypes.byref(view(seqs=seqs, seq_pages=1))
+        assert fa.fa_cache_workspace_size(c, 1) == 0
+        assert fa.fa_cache_free(c, G, 1, G, 1 << 40, 0) == fa.FA_ERR_UNSUPPORTED
+        assert fa.fa_paged_workspace_size(c, 1, 1, 4, 0) == 0
+
+
+@pytest.mark.gpu
+def test_write_of_almost_2_31_rows():
+    """The rows of a skipped sequence, up to the largest count, and one that is written."""
+    import torch
+    total = (1 << 31) - 1
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB free")
+    cache = fa.PagedCache.new(1, 4, 1, 16, 16, 2, 2)
+    pos = cache.extend(ints([0]), 3)
+    new = torch.empty(total, 1, 16, dtype=torch.bfloat16, device="cuda")
+    new[-3:] = torch.arange(3, device="cuda").bfloat16()[:, None, None] + 1
+    cache.write(0, new, new, ints([1, 0]), torch.cat([ints([-1]), pos]),
+                ints([0, total - 3, total]))
+    cache.check()
+    assert cache.k[0, 0, 0, :4, 0].tolist() == [1, 2, 3, 0] and not cache.k[0, 1:].any()
