@@ -352,11 +352,12 @@ cudaError_t launch_simt_d(const PagedArgs& a, bool pre, cudaStream_t st) {
 // every warp at it, a batch of 128 spent 20 us there), and per piece a warp
 // issues two shuffles, a load and d / 32 multiply-adds.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinBlocksPerSm = 4;
 constexpr int kJoinMaxRows = 16;
 constexpr int kChunk = 8;              // at most 16; 10 spilled and took 1 us more
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 4) 
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocksPerSm)
     join_kernel(const __grid_constant__ PagedArgs a, const int rows) {
   constexpr int kPer = D >= 32 ? D / 32 : 1;
   struct RowPieces {
@@ -502,10 +503,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
 
 template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, cudaStream_t st) {
-  // as many blocks as are resident at once (four an SM), then rows that share a block's set-up
-  const long long all = (long long)a.B * a.c.Hkv * a.TG;
+  // as many blocks as are resident at once, then rows that share a block's set-up
+  const long long all = (long long)a.B * a.c.Hkv * a.TG, resident = kJoinBlocksPerSm * a.own.sms;
   int rows = 1;
-  while (rows < kJoinMaxRows && all > 592 * rows) rows *= 2;
+  while (rows < kJoinMaxRows && all > resident * rows) rows *= 2;
   const dim3 grid((a.c.Hkv * a.TG + rows - 1) / rows, a.B);
   return launch_chained(join_kernel<T, D>, grid, kJoinWarps * 32, 0, st, true, a, rows);
 }
