@@ -119,7 +119,6 @@ Family pre_family(const PagedArgs& a) {
 // packed rows each, over `keys` keys at most. It depends on sizes and types only, so the
 // workspace query and the call agree.
 Phase divide(const CacheView& v, Family kind, int groups, int rows, long long keys, int sms) {
-  if (rows < 1) rows = 1;    // an empty call launches nothing, but its workspace may be asked for
   Phase p;
   p.sms = sms;
   int per = 1;           // streams of a block
@@ -365,6 +364,7 @@ fa_status fa_cache_compact(const fa_cache* cache, void* workspace, size_t worksp
 size_t fa_paged_workspace_size(const fa_cache* cache, int B, int T, int Hq, int shared) {
   CacheView v;
   if (view_of(cache, v) != FA_OK || check_fwd(v, B, T, Hq, shared) != FA_OK) return 0;
+  if (B == 0 || T == 0) return kPartialAlign;           // launches nothing, and there is no plan
   PagedArgs a;
   sizes(a, v, B, T, Hq, shared);
   if (!plan(a, sm_count())) return 0;

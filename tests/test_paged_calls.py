@@ -406,3 +406,11 @@ def test_write_of_almost_2_31_rows():
                 ints([0, total - 3, total]))
     cache.check()
     assert cache.k[0, 0, 0, :4, 0].tolist() == [1, 2, 3, 0] and not cache.k[0, 1:].any()
+
+
+def test_empty_calls_of_many_heads():
+    """Sizes whose products pass 32 bits where a factor is 0."""
+    heads = 1 << 20
+    c = ctypes.byref(view(Hkv=heads, d=16, page_stride=heads * 16 * 16))
+    for B, T in ((65535, 0), (0, 1 << 18)):
+        assert 0 < fa.fa_paged_workspace_size(c, B, T, heads, 0) < 1 << 20
