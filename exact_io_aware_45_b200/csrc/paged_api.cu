@@ -89,13 +89,16 @@ fa_status check_ws(const CacheView& v, int n, const void* ws, size_t bytes) {
 
 // Kernels of a phase: bf16 with d of 64 or 128 runs on the tensor cores, all else
 // on the CUDA cores. There the kernel tiled in registers takes 64 rows at once, the other up
-// to four: 64 sequences of 8 rows and 8 heads behind 4,096 tokens (fp32, d 128) take 191 us with
-// the first and 555 with the second, 32 decoding sequences of 8 rows (bf16, d 32) 14 and 18, but 8
-// of 5 rows and 8 heads 41 and 38. The mma.sync kernel reads K and V once per 16 or 24 packed rows
+// to four: 64 sequences of 4 rows and 8 heads behind 4,096 tokens (fp32, d 128, 256 rows of the
+// prefix) take 157 us with the first and 232 with the second, 16 of 16 rows and 4,000 tokens 329
+// and 361. For 5 to 8 rows the second, in tiles of four, would be quicker: the same with 6 rows 319
+// and 189, 32 sequences of 8 rows and 20 to 200 tokens (bf16, d 32) 16 and 14, 8 of 5 rows and 100
+// to 4,000 (fp32, d 64) 48 and 31. The mma.sync kernel reads K and V once per 16 or 24 packed rows
 // and is quick with short sequences; the tcgen05 kernel takes 128 or 256 rows at once, which
 // costs an item more to begin and end. Two row tiles (25 to 32 rows) of d 128 bind the first by
 // its work, so the second has them where a sequence may be long (`keys`: what its table can
-// hold): 64 sequences of 20 to 300 tokens take 29 and 43 us, 32 of 100 to 2,000 37 and 44, 80 of
+// hold, since no length is known on the host: a table wider than its sequences is taken for long
+// ones): 64 sequences of 20 to 300 tokens take 29 and 43 us, 32 of 100 to 2,000 37 and 44, 80 of
 // 1,562 (behind 2,144 shared) 285 and 200, 8 of 8,192 91 and 66. At d 64 they are level.
 // Where nothing can be long, up to 64 rows are quicker in tiles of 16 or 24: 61 sequences of
 // 40 rows and 8 heads with 1 to 49 tokens behind 128 shared take 41 us, 74 with an item each.
@@ -188,8 +191,11 @@ bool plan(PagedArgs& a, int sms) {
   a.own = divide(a.c, own_family(a), a.B * a.c.Hkv, a.TG, keys - a.shared, sms);
   if (a.shared) a.pre = divide(a.c, pre_family(a), a.c.Hkv, a.B * a.TG, a.shared, sms);
   // The tcgen05 kernel leaves the memory idle and the mma.sync kernel the tensor cores: they
-  // run side by side on different SMs. A tile of 256 rows takes an SM 2.2 us, 8 KB of an own
-  // stream 0.14 us.
+  // run side by side on different SMs. A tile of 256 rows takes an SM 2.2 us at d 128, 8 KB of an
+  // own stream 0.14 us: 16, and 8 for 128 rows. At d 64 the tiles of both are half the work. 128
+  // sequences with up to 2,048 tokens of their own behind 16,384 take 121 us (d 128) and 69 (d 64)
+  // with 16, 144 and 74 with 12, 184 and 91 with 8, 119 and 87 with 22; 24 of them 43 and 33 with
+  // 8, 58 and 30 with 4, 39 and 33 with 11.
   if (a.shared && pre_family(a) == kTc && own_family(a) == kMma)
     a.pre.yield = a.pre.rows == kTcRows ? 8 : 16;
   const long long most = keys / 16 + 8;

@@ -10,8 +10,8 @@
 // multiply-adds. Rows of K, V and Q are padded by 16 bytes:
 // eight keys (or four rows) read side by side fall into different banks.
 //
-// 64 sequences of 4 rows and 8 heads behind 4,096 tokens (fp32, d 128, 4.3 GFLOP) take 183 us in
-// all, 555 by simt_kernel; 128 of 8 rows and 4 heads behind 8,192 (d 64, 8.6 GFLOP) 272. The FMA
+// 64 sequences of 4 rows and 8 heads behind 4,096 tokens (fp32, d 128, 4.3 GFLOP) take 157 us in
+// all, 232 by simt_kernel; 128 of 8 rows and 4 heads behind 8,192 (d 64, 8.6 GFLOP) 278. The FMA
 // pipe is active in 48 % of the cycles, the scheduler issues in 62 %: three warps each, which the
 // registers allow, do not hide all latency.
 #include <cuda_bf16.h>

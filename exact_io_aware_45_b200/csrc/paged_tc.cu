@@ -23,8 +23,12 @@
 //
 // The running maximum is a reference that moves only when a tile exceeds it by 2^8 (the
 // recurrence holds for any reference), so most tiles leave the accumulator alone.
-// P is rounded to bf16 for the second product (the row sum takes it unrounded);
-// sums, statistics and O stay in fp32.
+// P is rounded to bf16 for the second product (the row sum takes it unrounded); sums, statistics
+// and O stay in fp32. The rounding of P is of the size of O's own: together they are off by 2.3e-3
+// (relative norm against 64 bits, 1,000 random keys), O's alone by 1.7e-3. A second number for the
+// rest of P, as in paged_mma.cu, gives 1.7e-3 too, and room for it is there (the lower half of
+// S), but the products and the softmax are the bound here: 256 rows over 8 sequences of 4,096 tokens
+// take 76 us instead of 63, a batch of 64 behind 4,096 tokens 30 instead of 26.
 #include <math.h>
 
 #include "paged_sched.cuh"

@@ -384,7 +384,14 @@ fa_status fa_debug_set_stall(int kernels, long long wait_cycles);
  * contiguous), so K and V may be two halves of one tensor or the layers may
  * lie inside the pages. K, V 16-byte aligned; the int32 arrays 4-byte.
  * page_size in {16, 32, 64, 128}, d in {16, 32, 64, 128}, dtype FA_F32 or
- * FA_BF16; K and V may exceed 2^31 elements.
+ * FA_BF16; K and V may exceed 2^31 elements. FA_ERR_UNSUPPORTED: 2^28 pages, 2^16
+ * layers, a page of 2^30 bytes in a layer, a table of 2^30 tokens for a sequence or of
+ * 2^31 - 65,536 entries in all, or more of any.
+ *
+ * A sequence is shortened by no call, nor by lowering lens: the pages behind the new
+ * length would stay in its table, and extend would write over their entries, which loses
+ * them. Tokens that may have to be taken back (drafts) go to a fork of the sequence,
+ * which is freed if they are refused and takes its place if not.
  *
  * What the device finds wrong in lists of slots and pages (a slot or page out
  * of range, one named twice, no free page left, a sequence past seq_pages
@@ -475,7 +482,10 @@ fa_status fa_cache_compact(const fa_cache* cache, void* workspace, size_t worksp
  * inconsistent state gives wrong results but no access outside the cache.
  * workspace: fa_paged_workspace_size bytes, device, 16-byte aligned, no
  * initial value; one call at a time. A bounded wait that runs out is reported
- * through cache->err (FA_ERR_TIMEOUT). Deterministic.
+ * through cache->err (FA_ERR_TIMEOUT). Deterministic. Sums and statistics are fp32;
+ * with bf16, d of 64 or 128 and many rows (T * Hq / Hkv, or B times as many in a shared
+ * prefix) the probabilities of the second product are rounded to bf16.
+ * FA_ERR_UNSUPPORTED: B > 65,535, B * T * Hq >= 2^28 or T * Hq / Hkv >= 2^20.
  */
 fa_status fa_fwd_paged(const fa_cache* cache, int layer, const void* Q, void* O, float* LSE,
                        const int* seqs, int B, int T, int Hq, float scale, int causal,
